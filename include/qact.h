@@ -396,6 +396,124 @@ int delta_cosine(const uint16_t* d_new, const uint16_t* d_prev, int64_t n, doubl
                  void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * qlinear_bf16: the linear of a few bf16 rows against an NVFP4 weight,
+ * without quantizing the rows (6Bit-Diffusion, Table 2: 4-bit weights): a
+ * conditioning vector's modulation, one token of each stream.
+ *   y[m][n] = w_ts sum_k x[m][k] W[n][k] (+ bias[n]) (-> GELU-tanh)
+ * x bf16 [M][ldx] (16-byte aligned, ldx % 8 == 0, ldx >= K), W NVFP4 [N][K]
+ * (w_q 16-byte aligned, w_s of any alignment), bias, y, out and epi as for
+ * qlinear_nvfp4.  0 <= M <= QA_ROWS_MAX (QA_ESHAPE otherwise: quantize more
+ * rows and use qlinear_nvfp4 or qlinear_int8); N, K as there.  Products of
+ * a value and a 4-bit element are exact and summed in float32; a group's
+ * scale is applied to the sum of its 16 products.  The weight's group
+ * scales must be numbers (codes 0x00..0x7E, as act_quant writes them).  No workspace. */
+#define QA_ROWS_MAX 32
+int qlinear_bf16(const uint16_t* x, int64_t ldx, const uint8_t* w_q, const uint8_t* w_s,
+                 const float* w_ts, int64_t M, int64_t N, int64_t K, const uint16_t* bias, void* y,
+                 int64_t ldy, qa_out out, qa_epi epi, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * qk_norm_rope: the norm of each query and key head and its rotation by the
+ * token's position, in one pass, between a block's QKV linear and its
+ * attention.
+ *   q bf16 [M][ldq], head h in columns h D .. h D + D - 1 (Hq heads); k
+ *   likewise (Hk heads); either may be NULL with no heads.
+ *   norm  QA_NORM_NONE; QA_NORM_RMS x / sqrt(mean x^2 + eps) w + b;
+ *         QA_NORM_LAYER (x - mean) / sqrt(var + eps) w + b, over a head's D
+ *         elements; w, b bf16 [D], one each for queries and keys, NULL: 1 and 0
+ *         (w and b must be NULL for QA_NORM_NONE).
+ *   rope  QA_ROPE_NONE; QA_ROPE_PAIRS turns elements (2 i, 2 i + 1),
+ *         QA_ROPE_HALVES (i, i + D / 2): (u, v) -> (u cos - v sin,
+ *         v cos + u sin) with cos, sin f32 [P][D / 2] at row pos[m] (int32
+ *         [M]; NULL: m), entry i.  A token whose position lies outside
+ *         0 .. P - 1 (-1 for the text tokens of a joint sequence) is not turned.
+ * float32 throughout, one rounding to bf16.  q_out, k_out bf16 [M][ldqo],
+ * [M][ldko]; each may be its input itself (same pointer and stride); no
+ * other overlap.  All bf16 pointers 16-byte aligned, strides multiples of 8;
+ * cos, sin and pos 4-byte aligned.  D a multiple of 16, 16 .. 256; eps >= 0;
+ * 0 <= M < 2^24, M (Hq + Hk) < 2^26.
+ * ------------------------------------------------------------------------ */
+typedef enum { QA_NORM_NONE = 0, QA_NORM_RMS = 1, QA_NORM_LAYER = 2 } qa_norm;
+typedef enum { QA_ROPE_NONE = 0, QA_ROPE_PAIRS = 1, QA_ROPE_HALVES = 2 } qa_rope;
+int qk_norm_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int64_t ldk, int Hk,
+                 int64_t M, int D, qa_norm norm, const uint16_t* q_w, const uint16_t* q_b,
+                 const uint16_t* k_w, const uint16_t* k_b, float eps, qa_rope rope,
+                 const float* cos, const float* sin, int64_t P, const int32_t* pos,
+                 uint16_t* q_out, int64_t ldqo, uint16_t* k_out, int64_t ldko, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A key/value cache in NVFP4 (9/16 byte per element) and attention over it,
+ * for a rollout that keeps the keys and values of earlier frames or tokens.
+ *
+ * Cache: pages of `page` tokens (a power of two, 16 .. 1024) for H heads of
+ * D elements (a multiple of 16, 16 .. 256), keys and values apart:
+ *   k_q, v_q u8 [pages][H][page][D/2], k_s, v_s u8 [pages][H][page][D/16]
+ *   (codes and E4M3 group scales as act_quant writes them, the groups along
+ *   a head; 16-byte aligned), k_ts, v_ts f32 device scalars, the tensor scales
+ *   (calibrated: a value beyond 2688 ts saturates).
+ *   table int32 [B][max_pages]: the token at position p of stream b is in
+ *   slot p % page of page table[b][p / page].  A position past the table or
+ *   an entry outside 0 .. pages - 1 has no slot.
+ * Streams may share pages that are only read.
+ *
+ * kv4_append encodes k, v bf16 [B T][ldk], [B T][ldv] (token t of stream b in
+ *   row b T + t, head h in columns h D ..; 16-byte aligned, strides multiples
+ *   of 8, finite values) at positions start[b] .. start[b] + count[b] - 1
+ *   (int32 [B]; count NULL: T; the rows behind count[b] are not read).  The
+ *   bytes are those of act_quant with QA_TSCALE_GIVEN.  Tokens without a slot
+ *   are dropped; every other slot stays as it was.
+ * kv4_read decodes the same positions into k, v (rows behind count[b] and
+ *   tokens without a slot are left as they were).
+ *   0 <= B, T; B T < 2^24; B T H D < 2^34.
+ *
+ * attn_kv4: q bf16 [B Lq][ldq] (Hq heads, head h attends with head
+ *   h / (Hq / H) of the cache), o likewise;
+ *     o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q . k_j)
+ *   over the positions j < lens[b] (int32 [B]; clamped to the table) that
+ *   have a slot.  q_lens int32 [B] (NULL: Lq): stream b has q_lens[b] query
+ *   rows; the rows behind them are neither read nor written.  causal != 0:
+ *   the last query row stands at position lens[b] - 1 and a row sees no
+ *   position after its own.  A row that sees nothing gives zeros.  Slots
+ *   that are not seen may hold any bytes.
+ *   D 64 or 128; Hq a multiple of H; scale > 0; B Lq Hq < 2^26.
+ *   ws: with attn_kv4_workspace() bytes a call with few query rows splits
+ *   the keys over more workgroups; less (also none) splits less.  The sums
+ *   are made in an order that the sizes and ws_bytes decide.
+ * ------------------------------------------------------------------------ */
+int kv4_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, int64_t B,
+               int64_t T, int H, int D, uint8_t* k_q, uint8_t* k_s, uint8_t* v_q, uint8_t* v_s,
+               const float* k_ts, const float* v_ts, int64_t pages, int page,
+               const int32_t* table, int64_t max_pages, const int32_t* start,
+               const int32_t* count, hipStream_t stream);
+int kv4_read(uint16_t* k, int64_t ldk, uint16_t* v, int64_t ldv, int64_t B, int64_t T, int H,
+             int D, const uint8_t* k_q, const uint8_t* k_s, const uint8_t* v_q,
+             const uint8_t* v_s, const float* k_ts, const float* v_ts, int64_t pages, int page,
+             const int32_t* table, int64_t max_pages, const int32_t* start, const int32_t* count,
+             hipStream_t stream);
+size_t attn_kv4_workspace(int64_t B, int64_t Lq, int Hq, int H, int D, int64_t max_len);
+int attn_kv4(const uint16_t* q, int64_t ldq, int64_t B, int64_t Lq, int Hq, int H, int D,
+             const uint8_t* k_q, const uint8_t* k_s, const uint8_t* v_q, const uint8_t* v_s,
+             const float* k_ts, const float* v_ts, int64_t pages, int page,
+             const int32_t* table, int64_t max_pages, const int32_t* lens, const int32_t* q_lens,
+             int causal, float scale, uint16_t* o, int64_t ldo, void* ws, size_t ws_bytes,
+             hipStream_t stream);
+
+/* attn_cross: attention of bf16 queries to an encoder's states of another
+ * length (a video block's tokens to the prompt's).  q, o as for attn_kv4; k,
+ * v bf16 [B Lk][ldk], [B Lk][ldv] (state j of sequence b in row b Lk + j,
+ * head h in columns h D ..; 16-byte aligned, strides multiples of 8).  A
+ * row of sequence b sees the states j < k_lens[b] (int32 [B]; NULL: Lk;
+ * clamped to Lk) with mask[b][j] != 0 (u8 [B][Lk]; NULL: all).  States that
+ * are not seen may hold any bits, NaN included.  A row that sees none gives
+ * zeros.  D 64 or 128; Hq a multiple of Hkv; scale > 0; B Lq Hq < 2^26,
+ * B Lk < 2^26.  ws as for attn_kv4. */
+size_t attn_cross_workspace(int64_t B, int64_t Lq, int64_t Lk, int Hq, int Hkv, int D);
+int attn_cross(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v,
+               int64_t ldv, int64_t B, int64_t Lq, int64_t Lk, int Hq, int Hkv, int D,
+               const int32_t* k_lens, const uint8_t* mask, float scale, uint16_t* o, int64_t ldo,
+               void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Host-side decisions (pure functions on HOST arrays; no GPU work).
  *
  * dmpq_mask (abstract: NVFP4 for temporally stable layers, INT8 for

@@ -13,6 +13,9 @@ LIB_PATH = os.path.join(HERE, "libqact.so")
 NVFP4, INT8 = 0, 1
 OUT_BF16, OUT_F32 = 0, 1
 EPI_NONE, EPI_GELU_TANH = 0, 1
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
+ROPE_NONE, ROPE_PAIRS, ROPE_HALVES = 0, 1, 2
+ROWS_MAX = 32                        # QA_ROWS_MAX
 TSCALE_GIVEN = 1
 AMAX_GIVEN = 2
 NOALLOC_SCRATCH_BYTES = 64 << 20     # QA_NOALLOC_SCRATCH_BYTES
@@ -29,6 +32,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_I = ctypes.c_int
 
 _SIGS = {
     "qa_strerror": (ctypes.c_char_p, [ctypes.c_int]),
@@ -82,6 +86,19 @@ _SIGS = {
     "qa_set_gate": (ctypes.c_int, [_P, ctypes.c_uint32]),
     "qa_decide_step": (ctypes.c_int, [_P, _P, _P, ctypes.c_double, ctypes.c_double, ctypes.c_int,
                                       ctypes.c_int, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "qlinear_bf16": (_I, [_P, _I64, _P, _P, _P, _I64, _I64, _I64, _P, _P, _I64, _I, _I, _P]),
+    "qk_norm_rope": (_I, [_P, _I64, _I, _P, _I64, _I, _I64, _I, _I, _P, _P, _P, _P, ctypes.c_float,
+                          _I, _P, _P, _I64, _P, _P, _I64, _P, _I64, _P]),
+    "kv4_append": (_I, [_P, _I64, _P, _I64, _I64, _I64, _I, _I, _P, _P, _P, _P, _P, _P, _I64, _I,
+                        _P, _I64, _P, _P, _P]),
+    "kv4_read": (_I, [_P, _I64, _P, _I64, _I64, _I64, _I, _I, _P, _P, _P, _P, _P, _P, _I64, _I,
+                      _P, _I64, _P, _P, _P]),
+    "attn_kv4_workspace": (_SZ, [_I64, _I64, _I, _I, _I, _I64]),
+    "attn_kv4": (_I, [_P, _I64, _I64, _I64, _I, _I, _I, _P, _P, _P, _P, _P, _P, _I64, _I, _P, _I64,
+                      _P, _P, _I, ctypes.c_float, _P, _I64, _P, _SZ, _P]),
+    "attn_cross_workspace": (_SZ, [_I64, _I64, _I64, _I, _I, _I]),
+    "attn_cross": (_I, [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _I, _I, _I, _P, _P,
+                        ctypes.c_float, _P, _I64, _P, _SZ, _P]),
     "qa_gamma_from_sums": (ctypes.c_double, [_P]),
     "qa_rel_l2_from_sums": (ctypes.c_double, [_P]),
     "qa_rel_err_from_sums": (ctypes.c_double, [_P]),
@@ -358,6 +375,180 @@ def delta_cosine(d_new, d_prev, sums3, ws, n=None, stream=None):
     n = d_new.numel() if n is None else n
     _check("delta_cosine", lib().delta_cosine(_ptr(d_new), _ptr(d_prev), n, _ptr(sums3),
                                               _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+# ------------------------------------ bf16 rows, attention and its inputs --
+
+def _on(dtype, *tensors):
+    """Every tensor given (None: not given) is of this dtype, has unit steps
+    in its last dimension and is on the current device."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is None:
+            continue
+        if t.dtype != dtype and not (dtype == torch.bfloat16 and t.dtype == torch.int16):
+            raise ValueError(f"expected a {dtype} tensor, got {t.dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+        if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
+            raise ValueError("a tensor's last dimension must be contiguous")
+
+
+def _whole(*tensors):
+    for t in tensors:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("a cache, table or table-like tensor must be contiguous")
+
+
+def _rows(t, rows, width, name):
+    """Row stride of a 2-D tensor of at least rows x width elements."""
+    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < width:
+        raise ValueError(f"{name}: needs shape [{rows}, {width}], got {tuple(t.shape)}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (t.shape[1] + 7) // 8 * 8)
+
+
+def _sized(t, n, name):
+    if t is not None and t.numel() < n:
+        raise ValueError(f"{name}: needs {n} elements, got {t.numel()}")
+
+
+def qlinear_bf16(x, w_q, w_s, w_ts, y, M, N, K, bias=None, out=OUT_BF16, epi=EPI_NONE, ldx=None,
+                 ldy=None, stream=None):
+    """The linear of M <= ROWS_MAX bf16 rows x [M, ldx] against an NVFP4 weight."""
+    import torch
+    _on(torch.bfloat16, x, bias)
+    _on(torch.uint8, w_q, w_s)
+    _on(torch.float32, w_ts)
+    _on(torch.float32 if out == OUT_F32 else torch.bfloat16, y)
+    ldx = _rows(x, M, K, "x") if ldx is None else ldx
+    ldy = max(y.stride(0), y.shape[1]) if ldy is None else ldy
+    _check("qlinear_bf16", lib().qlinear_bf16(
+        _ptr(x), ldx, _ptr(w_q), _ptr(w_s), _ptr(w_ts), M, N, K, _ptr(bias), _ptr(y), ldy, out,
+        epi, _stream(stream)))
+
+
+def qk_norm_rope(q, k, q_out, k_out, M, Hq, Hk, D, norm=NORM_LAYER, q_w=None, q_b=None, k_w=None,
+                 k_b=None, eps=1e-6, rope=ROPE_NONE, cos=None, sin=None, pos=None, stream=None):
+    """Norm of every query head of q [M, Hq * D] and key head of k [M, Hk * D]
+    (bf16, rows of any stride; None without heads) and their rotation by the
+    float32 tables cos, sin [P, D / 2] at row pos[m] (int32; None: m; outside
+    the table: not turned) into q_out and k_out, which may be q and k."""
+    import torch
+    _on(torch.bfloat16, q, k, q_out, k_out, q_w, q_b, k_w, k_b)
+    _on(torch.float32, cos, sin)
+    _on(torch.int32, pos)
+    ld = [_rows(t, M, h * D, n) if t is not None else 0
+          for t, h, n in ((q, Hq, "q"), (k, Hk, "k"), (q_out, Hq, "q_out"), (k_out, Hk, "k_out"))]
+    for t in (q_w, q_b, k_w, k_b):
+        _sized(t, D, "a norm's weight or bias")
+    _sized(pos, M, "pos")
+    _whole(cos, sin, pos)
+    P = 0
+    if cos is not None and sin is not None:
+        P = min(cos.numel(), sin.numel()) // (D // 2)
+    _check("qk_norm_rope", lib().qk_norm_rope(
+        _ptr(q), ld[0], Hq, _ptr(k), ld[1], Hk, M, D, norm, _ptr(q_w), _ptr(q_b), _ptr(k_w),
+        _ptr(k_b), eps, rope, _ptr(cos), _ptr(sin), P, _ptr(pos), _ptr(q_out), ld[2],
+        _ptr(k_out), ld[3], _stream(stream)))
+
+
+def _kv4(k_q, k_s, v_q, v_s, k_ts, v_ts, table, B):
+    """(H, D, pages, page, max_pages) of a cache, after its checks."""
+    import torch
+    _on(torch.uint8, k_q, k_s, v_q, v_s)
+    _on(torch.float32, k_ts, v_ts)
+    _on(torch.int32, table)
+    _whole(k_q, k_s, v_q, v_s, table)
+    if k_q.dim() != 4 or table.dim() != 2:
+        raise ValueError("a cache part is [pages, H, page, D / 2], a table [B, max_pages]")
+    pages, H, page, half = k_q.shape
+    D = 2 * half
+    if v_q.shape != k_q.shape or k_s.shape != (pages, H, page, D // 16) or v_s.shape != k_s.shape:
+        raise ValueError("the cache parts' shapes do not fit each other")
+    if table.shape[0] < B:
+        raise ValueError(f"table: needs {B} rows, got {table.shape[0]}")
+    return H, D, pages, page, table.shape[1]
+
+
+def kv4_append(k, v, k_q, k_s, v_q, v_s, k_ts, v_ts, table, start, B, T, count=None, stream=None):
+    """Encode keys and values (bf16 [B * T, H * D], rows of any stride) into
+    the NVFP4 cache at positions start[b] .. start[b] + count[b] - 1 (int32;
+    count None: T)."""
+    import torch
+    H, D, pages, page, mp = _kv4(k_q, k_s, v_q, v_s, k_ts, v_ts, table, B)
+    _on(torch.bfloat16, k, v)
+    _on(torch.int32, start, count)
+    _sized(start, B, "start")
+    _sized(count, B, "count")
+    _check("kv4_append", lib().kv4_append(
+        _ptr(k), _rows(k, B * T, H * D, "k"), _ptr(v), _rows(v, B * T, H * D, "v"), B, T, H, D,
+        _ptr(k_q), _ptr(k_s), _ptr(v_q), _ptr(v_s), _ptr(k_ts), _ptr(v_ts), pages, page,
+        _ptr(table), mp, _ptr(start), _ptr(count), _stream(stream)))
+
+
+def kv4_read(k, v, k_q, k_s, v_q, v_s, k_ts, v_ts, table, start, B, T, count=None, stream=None):
+    """Decode the positions that kv4_append would write into k and v (bf16)."""
+    import torch
+    H, D, pages, page, mp = _kv4(k_q, k_s, v_q, v_s, k_ts, v_ts, table, B)
+    _on(torch.bfloat16, k, v)
+    _on(torch.int32, start, count)
+    _sized(start, B, "start")
+    _sized(count, B, "count")
+    _check("kv4_read", lib().kv4_read(
+        _ptr(k), _rows(k, B * T, H * D, "k"), _ptr(v), _rows(v, B * T, H * D, "v"), B, T, H, D,
+        _ptr(k_q), _ptr(k_s), _ptr(v_q), _ptr(v_s), _ptr(k_ts), _ptr(v_ts), pages, page,
+        _ptr(table), mp, _ptr(start), _ptr(count), _stream(stream)))
+
+
+def attn_kv4_workspace(B, Lq, Hq, H, D, max_len):
+    return lib().attn_kv4_workspace(B, Lq, Hq, H, D, max_len)
+
+
+def attn_kv4(q, k_q, k_s, v_q, v_s, k_ts, v_ts, table, lens, o, B, Lq, Hq, q_lens=None,
+             causal=True, scale=None, ws=None, stream=None):
+    """Attention of q [B * Lq, Hq * D] (bf16, rows of any stride) over the
+    first lens[b] positions of each stream's NVFP4 cache into o; scale None:
+    1 / sqrt(D)."""
+    import torch
+    H, D, pages, page, mp = _kv4(k_q, k_s, v_q, v_s, k_ts, v_ts, table, B)
+    _on(torch.bfloat16, q, o)
+    _on(torch.int32, lens, q_lens)
+    _sized(lens, B, "lens")
+    _sized(q_lens, B, "q_lens")
+    _on(torch.uint8, ws)
+    _check("attn_kv4", lib().attn_kv4(
+        _ptr(q), _rows(q, B * Lq, Hq * D, "q"), B, Lq, Hq, H, D, _ptr(k_q), _ptr(k_s), _ptr(v_q),
+        _ptr(v_s), _ptr(k_ts), _ptr(v_ts), pages, page, _ptr(table), mp, _ptr(lens),
+        _ptr(q_lens), 1 if causal else 0, D ** -0.5 if scale is None else scale, _ptr(o),
+        _rows(o, B * Lq, Hq * D, "o"), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def attn_cross_workspace(B, Lq, Lk, Hq, Hkv, D):
+    return lib().attn_cross_workspace(B, Lq, Lk, Hq, Hkv, D)
+
+
+def attn_cross(q, k, v, o, B, Lq, Lk, Hq, Hkv, D, k_lens=None, mask=None, scale=None, ws=None,
+               stream=None):
+    """Attention of q [B * Lq, Hq * D] to an encoder's states k, v
+    [B * Lk, Hkv * D] (bf16, rows of any stride) into o: the states before
+    k_lens[b] (int32) with mask[b][j] != 0 (uint8 or bool [B, Lk]); scale
+    None: 1 / sqrt(D)."""
+    import torch
+    if mask is not None and mask.dtype == torch.bool:
+        mask = mask.view(torch.uint8)
+    _on(torch.bfloat16, q, k, v, o)
+    _on(torch.int32, k_lens)
+    _on(torch.uint8, mask, ws)
+    _whole(mask)
+    _sized(k_lens, B, "k_lens")
+    _sized(mask, B * Lk, "mask")
+    w = Hkv * D
+    _check("attn_cross", lib().attn_cross(
+        _ptr(q), _rows(q, B * Lq, Hq * D, "q"), _ptr(k), _rows(k, B * Lk, w, "k"), _ptr(v),
+        _rows(v, B * Lk, w, "v"), B, Lq, Lk, Hq, Hkv, D, _ptr(k_lens), _ptr(mask),
+        D ** -0.5 if scale is None else scale, _ptr(o), _rows(o, B * Lq, Hq * D, "o"), _ptr(ws),
+        _nbytes(ws), _stream(stream)))
 
 
 # ------------------------------------------------------- host decisions --

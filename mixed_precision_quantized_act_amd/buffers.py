@@ -20,6 +20,14 @@ def empty_nvfp4(rows, K, device="cuda"):
             torch.empty((1,), dtype=torch.float32, device=device))
 
 
+def empty_kv4(pages, heads, page, D, device="cuda"):
+    """A key/value cache in NVFP4: (k_q, k_s, v_q, v_s), codes u8 [pages,
+    heads, page, D/2] and scales u8 [pages, heads, page, D/16]."""
+    torch = _torch()
+    part = lambda d: torch.empty((pages, heads, page, d), dtype=torch.uint8, device=device)
+    return part(D // 2), part(D // 16), part(D // 2), part(D // 16)
+
+
 def empty_int8_act(rows, K, device="cuda"):
     """(q i8 [rows, K], scale f32 [rows])."""
     torch = _torch()

@@ -28,6 +28,8 @@ namespace {
 // grid below 2^32 threads.
 constexpr int64_t kMaxRows = (int64_t)1 << 26;  // M, N
 constexpr int64_t kMaxK = (int64_t)1 << 23;
+constexpr int64_t kMaxLd = (int64_t)1 << 32;    // row stride of heads and of a few bf16 rows
+constexpr int64_t kMaxCache = (int64_t)1 << 44; // elements of a key/value cache part
 constexpr int64_t kMaxTiles = (int64_t)1 << 24; // 256 x 128 output tiles of one linear
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -37,6 +39,23 @@ size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return an && bn && x < y + bn && y < x + an;
+}
+
+// Whether columns [0, wa) of M rows of stride lda from a and columns [0, wb)
+// of M rows of stride ldb from b (2-byte elements) can meet.  Slices of one
+// row-major buffer at other columns do not; rows of other strides are taken
+// to meet where their extents do.
+bool rows_overlap(const void* a, int64_t lda, int64_t wa, const void* b, int64_t ldb, int64_t wb,
+                  int64_t Ma, int64_t Mb) {
+  if (Ma <= 0 || Mb <= 0 || wa <= 0 || wb <= 0) return false;
+  if (!overlap(a, (size_t)((Ma - 1) * lda + wa) * 2, b, (size_t)((Mb - 1) * ldb + wb) * 2))
+    return false;
+  if (lda != ldb) return true;
+  const int64_t d = ((int64_t)reinterpret_cast<uintptr_t>(b) - (int64_t)reinterpret_cast<uintptr_t>(a));
+  if (d % 2) return true;
+  int64_t r = (d / 2) % lda;
+  if (r < 0) r += lda;
+  return !(r >= wa && r + wb <= lda);
 }
 
 int hip_status(hipError_t e) { return e == hipSuccess ? QA_OK : QA_EHIP; }
@@ -671,6 +690,256 @@ int qa_set_gemm_events(hipEvent_t before, hipEvent_t after) {
 static double ratio0(double num, double den) {
   if (den == 0.0) return num == 0.0 ? 0.0 : INFINITY;
   return num / den;
+}
+
+// ------------------------------------- bf16 rows, attention and its inputs --
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int qlinear_bf16(const uint16_t* x, int64_t ldx, const uint8_t* w_q, const uint8_t* w_s,
+                 const float* w_ts, int64_t M, int64_t N, int64_t K, const uint16_t* bias, void* y,
+                 int64_t ldy, qa_out out, qa_epi epi, hipStream_t stream) {
+  if (!x || !w_q || !w_s || !w_ts) return QA_EINVAL;
+  if (int s = check_linear(M, N, K, y, ldy, out, epi)) return s;
+  if (M > QA_ROWS_MAX || ldx < K || ldx % 8 || ldx >= kMaxLd) return QA_ESHAPE;
+  if (!aligned16(x) || !aligned16(w_q) || !aligned4(w_ts) ||
+      (reinterpret_cast<uintptr_t>(bias) & 1u))
+    return QA_EALIGN;
+  const size_t ybytes = M && N ? (size_t)((M - 1) * ldy + N) * (out == QA_OUT_F32 ? 4 : 2) : 0;
+  const size_t xbytes = M ? (size_t)((M - 1) * ldx + K) * 2 : 0;
+  if (overlap(y, ybytes, x, xbytes) || overlap(y, ybytes, w_q, (size_t)(N * K / 2)) ||
+      overlap(y, ybytes, w_s, (size_t)(N * K / 16)) || overlap(y, ybytes, w_ts, 4) ||
+      (bias && overlap(y, ybytes, bias, (size_t)N * 2)))
+    return QA_EALIAS;
+  if (M == 0 || N == 0) return QA_OK;
+  const GemmOut o = {y, ldy, out == QA_OUT_F32, epi == QA_EPI_GELU_TANH, bias};
+  return hip_status(launch_qgemv(x, ldx, w_q, w_s, w_ts, M, N, K, o, stream));
+}
+
+// `rows` rows of H heads of D elements, of stride ld (no rows: p may be NULL)
+static int check_heads(const void* p, int64_t rows, int64_t ld, int H, int D) {
+  if (H == 0) return p ? QA_EINVAL : QA_OK;
+  if (!p && rows) return QA_EINVAL;
+  if ((int64_t)H * D >= kMaxK || ld < (int64_t)H * D || ld % 8 || ld >= kMaxLd) return QA_ESHAPE;
+  return aligned16(p) ? QA_OK : QA_EALIGN;
+}
+
+int qk_norm_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int64_t ldk, int Hk,
+                 int64_t M, int D, qa_norm norm, const uint16_t* q_w, const uint16_t* q_b,
+                 const uint16_t* k_w, const uint16_t* k_b, float eps, qa_rope rope,
+                 const float* cos, const float* sin, int64_t P, const int32_t* pos,
+                 uint16_t* q_out, int64_t ldqo, uint16_t* k_out, int64_t ldko,
+                 hipStream_t stream) {
+  if (norm != QA_NORM_NONE && norm != QA_NORM_RMS && norm != QA_NORM_LAYER) return QA_EINVAL;
+  if (rope != QA_ROPE_NONE && rope != QA_ROPE_PAIRS && rope != QA_ROPE_HALVES) return QA_EINVAL;
+  if (norm == QA_NORM_NONE && (q_w || q_b || k_w || k_b)) return QA_EINVAL;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return QA_EINVAL;
+  if (Hq < 0 || Hk < 0 || Hq + (int64_t)Hk == 0) return QA_EINVAL;
+  if (D < 16 || D > 256 || D % 16 || M < 0 || M >= (int64_t)1 << 24 ||
+      M * ((int64_t)Hq + Hk) >= (int64_t)1 << 26)
+    return QA_ESHAPE;
+  if (int s = check_heads(q, M, ldq, Hq, D)) return s;
+  if (int s = check_heads(k, M, ldk, Hk, D)) return s;
+  if (int s = check_heads(q_out, M, ldqo, Hq, D)) return s;
+  if (int s = check_heads(k_out, M, ldko, Hk, D)) return s;
+  if (rope == QA_ROPE_NONE ? (cos || sin || pos) : (P != 0 && (!cos || !sin))) return QA_EINVAL;
+  if (rope != QA_ROPE_NONE && P < 0) return QA_ESHAPE;
+  if (!aligned16(q_w) || !aligned16(q_b) || !aligned16(k_w) || !aligned16(k_b)) return QA_EALIGN;
+  if (!aligned4(cos) || !aligned4(sin) || !aligned4(pos)) return QA_EALIGN;
+  const int64_t wq = (int64_t)Hq * D, wk = (int64_t)Hk * D;
+  const bool q_in = q_out == q && ldqo == ldq, k_in = k_out == k && ldko == ldk;
+  if ((!q_in && rows_overlap(q_out, ldqo, wq, q, ldq, wq, M, M)) ||
+      (!k_in && rows_overlap(k_out, ldko, wk, k, ldk, wk, M, M)) ||
+      rows_overlap(q_out, ldqo, wq, k, ldk, wk, M, M) ||
+      rows_overlap(k_out, ldko, wk, q, ldq, wq, M, M) ||
+      rows_overlap(q_out, ldqo, wq, k_out, ldko, wk, M, M))
+    return QA_EALIAS;
+  if (M == 0) return QA_OK;
+  const QkArgs a = {q, ldq, k, ldk, M, Hq, Hk, D, norm, rope, q_w, q_b, k_w, k_b,
+                    eps, 1.0f / (float)D, cos, sin, P, pos, q_out, ldqo, k_out, ldko};
+  return hip_status(launch_qk_norm_rope(a, stream));
+}
+
+static int check_kv4(const Kv4Cache& c, int64_t B, int page) {
+  if (!c.k_ts || !c.v_ts || (!c.table && B && c.max_pages)) return QA_EINVAL;
+  if (c.pages && (!c.k_q || !c.k_s || !c.v_q || !c.v_s)) return QA_EINVAL;
+  if (c.H <= 0 || c.D < 16 || c.D > 256 || c.D % 16 || (int64_t)c.H * c.D >= kMaxK)
+    return QA_ESHAPE;
+  if (page < 16 || page > 1024 || (page & (page - 1))) return QA_ESHAPE;
+  if (c.pages < 0 || c.max_pages < 0 || c.pages >= (int64_t)1 << 31 ||
+      c.max_pages >= (int64_t)1 << 27 || B < 0)
+    return QA_ESHAPE;
+  if (c.pages > kMaxCache / ((int64_t)c.H * c.D * page)) return QA_ESHAPE;
+  if (!aligned16(c.k_q) || !aligned16(c.k_s) || !aligned16(c.v_q) || !aligned16(c.v_s) ||
+      !aligned4(c.k_ts) || !aligned4(c.v_ts) || !aligned4(c.table))
+    return QA_EALIGN;
+  return QA_OK;
+}
+
+static int log2_of(int page) {
+  int n = 0;
+  while ((1 << n) < page) ++n;
+  return n;
+}
+
+// the four cache arrays and their sizes
+struct Kv4Parts {
+  const void* p[4];
+  size_t n[4];
+  explicit Kv4Parts(const Kv4Cache& c) : p{c.k_q, c.k_s, c.v_q, c.v_s} {
+    const size_t rows = ((size_t)c.pages * c.H) << c.page_log2;
+    n[0] = n[2] = rows * (c.D / 2);
+    n[1] = n[3] = rows * (c.D / 16);
+  }
+  bool meet(const void* a, size_t an) const {
+    for (int i = 0; i < 4; ++i)
+      if (overlap(a, an, p[i], n[i])) return true;
+    return false;
+  }
+  bool meet_each_other() const {
+    for (int i = 0; i < 4; ++i)
+      for (int j = i + 1; j < 4; ++j)
+        if (overlap(p[i], n[i], p[j], n[j])) return true;
+    return false;
+  }
+};
+
+static int check_kv4_rows(const Kv4Cache& c, const void* k, int64_t ldk, const void* v,
+                          int64_t ldv, int64_t B, int64_t T, int page, const int32_t* start,
+                          const int32_t* count) {
+  if (!start && B) return QA_EINVAL;
+  if (int s = check_kv4(c, B, page)) return s;
+  if (T < 0 || B >= (int64_t)1 << 24 || T >= (int64_t)1 << 24 || B * T >= (int64_t)1 << 24 ||
+      B * T * c.H >= ((int64_t)1 << 34) / c.D)
+    return QA_ESHAPE;
+  if (int s = check_heads(k, B * T, ldk, c.H, c.D)) return s;
+  if (int s = check_heads(v, B * T, ldv, c.H, c.D)) return s;
+  if (!aligned4(start) || !aligned4(count)) return QA_EALIGN;
+  return QA_OK;
+}
+
+static size_t rows_bytes(int64_t rows, int64_t ld, int64_t width) {
+  return rows > 0 ? (size_t)((rows - 1) * ld + width) * 2 : 0;
+}
+
+int kv4_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, int64_t B,
+               int64_t T, int H, int D, uint8_t* k_q, uint8_t* k_s, uint8_t* v_q, uint8_t* v_s,
+               const float* k_ts, const float* v_ts, int64_t pages, int page,
+               const int32_t* table, int64_t max_pages, const int32_t* start,
+               const int32_t* count, hipStream_t stream) {
+  const Kv4Cache c = {k_q, k_s, v_q, v_s, k_ts, v_ts, pages, log2_of(page), H, D, table, max_pages};
+  if (int s = check_kv4_rows(c, k, ldk, v, ldv, B, T, page, start, count)) return s;
+  const Kv4Parts parts(c);
+  const int64_t w = (int64_t)H * D;
+  if (parts.meet_each_other() || parts.meet(k, rows_bytes(B * T, ldk, w)) ||
+      parts.meet(v, rows_bytes(B * T, ldv, w)) || parts.meet(table, (size_t)(B * max_pages) * 4) ||
+      parts.meet(start, (size_t)B * 4) || (count && parts.meet(count, (size_t)B * 4)) ||
+      parts.meet(k_ts, 4) || parts.meet(v_ts, 4))
+    return QA_EALIAS;
+  if (B * T == 0) return QA_OK;
+  return hip_status(launch_kv4_append(c, k, ldk, v, ldv, B, T, start, count, stream));
+}
+
+int kv4_read(uint16_t* k, int64_t ldk, uint16_t* v, int64_t ldv, int64_t B, int64_t T, int H,
+             int D, const uint8_t* k_q, const uint8_t* k_s, const uint8_t* v_q,
+             const uint8_t* v_s, const float* k_ts, const float* v_ts, int64_t pages, int page,
+             const int32_t* table, int64_t max_pages, const int32_t* start, const int32_t* count,
+             hipStream_t stream) {
+  const Kv4Cache c = {const_cast<uint8_t*>(k_q), const_cast<uint8_t*>(k_s),
+                      const_cast<uint8_t*>(v_q), const_cast<uint8_t*>(v_s), k_ts, v_ts, pages,
+                      log2_of(page), H, D, table, max_pages};
+  if (int s = check_kv4_rows(c, k, ldk, v, ldv, B, T, page, start, count)) return s;
+  const Kv4Parts parts(c);
+  const int64_t w = (int64_t)H * D;
+  const void* outs[2] = {k, v};
+  const size_t ob[2] = {rows_bytes(B * T, ldk, w), rows_bytes(B * T, ldv, w)};
+  for (int i = 0; i < 2; ++i)
+    if (parts.meet(outs[i], ob[i]) || overlap(outs[i], ob[i], table, (size_t)(B * max_pages) * 4) ||
+        overlap(outs[i], ob[i], start, (size_t)B * 4) ||
+        (count && overlap(outs[i], ob[i], count, (size_t)B * 4)) ||
+        overlap(outs[i], ob[i], k_ts, 4) || overlap(outs[i], ob[i], v_ts, 4))
+      return QA_EALIAS;
+  if (rows_overlap(k, ldk, w, v, ldv, w, B * T, B * T)) return QA_EALIAS;
+  if (B * T == 0) return QA_OK;
+  return hip_status(launch_kv4_read(c, k, ldk, v, ldv, B, T, start, count, stream));
+}
+
+static int check_attn(const AttnArgs& a, const void* ws, size_t ws_bytes) {
+  if (!(a.scale > 0.0f) || !std::isfinite(a.scale)) return QA_EINVAL;
+  if (a.D != 64 && a.D != 128) return QA_ESHAPE;
+  if (a.Hq <= 0 || a.Hkv <= 0 || a.Hq % a.Hkv || a.B < 0 || a.Lq < 0 ||
+      a.B >= (int64_t)1 << 24 || a.Lq >= (int64_t)1 << 26 || a.B * a.Lq >= (int64_t)1 << 26 ||
+      a.B * a.Lq * a.Hq >= (int64_t)1 << 26)
+    return QA_ESHAPE;
+  if (int s = check_heads(a.q, a.B * a.Lq, a.ldq, a.Hq, a.D)) return s;
+  if (int s = check_heads(a.o, a.B * a.Lq, a.ldo, a.Hq, a.D)) return s;
+  if (ws_bytes && !ws) return QA_EINVAL;
+  if (!aligned16(ws)) return QA_EALIGN;
+  const int64_t w = (int64_t)a.Hq * a.D, rows = a.B * a.Lq;
+  if (rows_overlap(a.o, a.ldo, w, a.q, a.ldq, w, rows, rows) ||
+      overlap(ws, ws_bytes, a.q, rows_bytes(rows, a.ldq, w)) ||
+      overlap(ws, ws_bytes, a.o, rows_bytes(rows, a.ldo, w)))
+    return QA_EALIAS;
+  return QA_OK;
+}
+
+size_t attn_kv4_workspace(int64_t B, int64_t Lq, int Hq, int H, int D, int64_t max_len) {
+  return attn_ws_bytes(B, Lq, Hq, H, D, max_len);
+}
+
+int attn_kv4(const uint16_t* q, int64_t ldq, int64_t B, int64_t Lq, int Hq, int H, int D,
+             const uint8_t* k_q, const uint8_t* k_s, const uint8_t* v_q, const uint8_t* v_s,
+             const float* k_ts, const float* v_ts, int64_t pages, int page,
+             const int32_t* table, int64_t max_pages, const int32_t* lens, const int32_t* q_lens,
+             int causal, float scale, uint16_t* o, int64_t ldo, void* ws, size_t ws_bytes,
+             hipStream_t stream) {
+  const Kv4Cache c = {const_cast<uint8_t*>(k_q), const_cast<uint8_t*>(k_s),
+                      const_cast<uint8_t*>(v_q), const_cast<uint8_t*>(v_s), k_ts, v_ts, pages,
+                      log2_of(page), H, D, table, max_pages};
+  const AttnArgs a = {q, ldq, o, ldo, B, Lq, Hq, H, D, scale};
+  if (!lens && B) return QA_EINVAL;
+  if (int s = check_kv4(c, B, page)) return s;
+  if (int s = check_attn(a, ws, ws_bytes)) return s;
+  if (!aligned4(lens) || !aligned4(q_lens)) return QA_EALIGN;
+  const Kv4Parts parts(c);
+  const void* outs[2] = {o, ws};
+  const size_t ob[2] = {rows_bytes(B * Lq, ldo, (int64_t)Hq * D), ws_bytes};
+  for (int i = 0; i < 2; ++i)
+    if (parts.meet(outs[i], ob[i]) || overlap(outs[i], ob[i], table, (size_t)(B * max_pages) * 4) ||
+        overlap(outs[i], ob[i], lens, (size_t)B * 4) ||
+        (q_lens && overlap(outs[i], ob[i], q_lens, (size_t)B * 4)) ||
+        overlap(outs[i], ob[i], k_ts, 4) || overlap(outs[i], ob[i], v_ts, 4))
+      return QA_EALIAS;
+  if (B * Lq == 0) return QA_OK;
+  return hip_status(launch_attn_kv4(a, c, lens, q_lens, causal != 0, ws, ws_bytes, stream));
+}
+
+size_t attn_cross_workspace(int64_t B, int64_t Lq, int64_t Lk, int Hq, int Hkv, int D) {
+  return attn_ws_bytes(B, Lq, Hq, Hkv, D, Lk);
+}
+
+int attn_cross(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v,
+               int64_t ldv, int64_t B, int64_t Lq, int64_t Lk, int Hq, int Hkv, int D,
+               const int32_t* k_lens, const uint8_t* mask, float scale, uint16_t* o, int64_t ldo,
+               void* ws, size_t ws_bytes, hipStream_t stream) {
+  const AttnArgs a = {q, ldq, o, ldo, B, Lq, Hq, Hkv, D, scale};
+  if (int s = check_attn(a, ws, ws_bytes)) return s;
+  if (Lk < 0 || Lk >= (int64_t)1 << 26 || B * Lk >= (int64_t)1 << 26) return QA_ESHAPE;
+  if (int s = check_heads(k, B * Lk, ldk, Hkv, D)) return s;
+  if (int s = check_heads(v, B * Lk, ldv, Hkv, D)) return s;
+  if (!aligned4(k_lens)) return QA_EALIGN;
+  const int64_t w = (int64_t)Hkv * D;
+  const size_t kb = rows_bytes(B * Lk, ldk, w), vb = rows_bytes(B * Lk, ldv, w);
+  const size_t ob = rows_bytes(B * Lq, ldo, (int64_t)Hq * D);
+  if (overlap(ws, ws_bytes, k, kb) || overlap(ws, ws_bytes, v, vb) ||
+      (k_lens && (overlap(ws, ws_bytes, k_lens, (size_t)B * 4) || overlap(o, ob, k_lens, (size_t)B * 4))) ||
+      (mask && (overlap(ws, ws_bytes, mask, (size_t)(B * Lk)) || overlap(o, ob, mask, (size_t)(B * Lk)))) ||
+      rows_overlap(o, ldo, (int64_t)Hq * D, k, ldk, w, B * Lq, B * Lk) ||
+      rows_overlap(o, ldo, (int64_t)Hq * D, v, ldv, w, B * Lq, B * Lk))
+    return QA_EALIAS;
+  if (B * Lq == 0) return QA_OK;
+  return hip_status(
+      launch_attn_cross(a, k, ldk, v, ldv, Lk, k_lens, mask, ws, ws_bytes, stream));
 }
 
 // ------------------------------------------------ device-side step control --

@@ -148,4 +148,65 @@ hipError_t launch_tdc(int mode, const uint16_t* in, const uint16_t* b, const uin
                       uint16_t* dst, int64_t n, double* sums, void* ws, hipStream_t stream,
                       uint32_t* amax_out = nullptr, const RingRoute* route = nullptr);
 
+// ---- bf16 rows against an NVFP4 weight (qgemv.hip); M <= QA_ROWS_MAX
+hipError_t launch_qgemv(const uint16_t* x, int64_t ldx, const uint8_t* w_q, const uint8_t* w_s,
+                        const float* w_ts, int64_t M, int64_t N, int64_t K, const GemmOut& o,
+                        hipStream_t stream);
+
+// ---- norm and rotation of query and key heads (qk_norm.hip)
+struct QkArgs {
+  const uint16_t* q;
+  int64_t ldq;
+  const uint16_t* k;
+  int64_t ldk, M;
+  int Hq, Hk, D;
+  int norm, rope;         // qa_norm, qa_rope
+  const uint16_t *q_w, *q_b, *k_w, *k_b;
+  float eps, inv_D;
+  const float *cos, *sin;
+  int64_t P;
+  const int32_t* pos;
+  uint16_t* q_out;
+  int64_t ldqo;
+  uint16_t* k_out;
+  int64_t ldko;
+};
+hipError_t launch_qk_norm_rope(const QkArgs& a, hipStream_t stream);
+
+// ---- the NVFP4 key/value cache (kv4.hip): pages [pages][H][page] of D/2
+// code bytes and D/16 scale bytes, keys and values apart
+struct Kv4Cache {
+  uint8_t *k_q, *k_s, *v_q, *v_s;
+  const float *k_ts, *v_ts;
+  int64_t pages;
+  int page_log2, H, D;
+  const int32_t* table;   // [B][max_pages]
+  int64_t max_pages;
+};
+hipError_t launch_kv4_append(const Kv4Cache& c, const uint16_t* k, int64_t ldk, const uint16_t* v,
+                             int64_t ldv, int64_t B, int64_t T, const int32_t* start,
+                             const int32_t* count, hipStream_t stream);
+hipError_t launch_kv4_read(const Kv4Cache& c, uint16_t* k, int64_t ldk, uint16_t* v, int64_t ldv,
+                           int64_t B, int64_t T, const int32_t* start, const int32_t* count,
+                           hipStream_t stream);
+
+// ---- attention (attn.hip)
+struct AttnArgs {
+  const uint16_t* q;
+  int64_t ldq;
+  uint16_t* o;
+  int64_t ldo;
+  int64_t B, Lq;
+  int Hq, Hkv, D;
+  float scale;
+};
+// the workspace that lets a call with few rows split the keys, keys <= L
+size_t attn_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L);
+hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4Cache& c, const int32_t* lens,
+                           const int32_t* q_lens, bool causal, void* ws, size_t ws_bytes,
+                           hipStream_t stream);
+hipError_t launch_attn_cross(const AttnArgs& a, const uint16_t* k, int64_t ldk, const uint16_t* v,
+                             int64_t ldv, int64_t Lk, const int32_t* k_lens, const uint8_t* mask,
+                             void* ws, size_t ws_bytes, hipStream_t stream);
+
 }  // namespace qact
