@@ -454,6 +454,7 @@ int qk_norm_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int6
  *   table int32 [B][max_pages]: the token at position p of stream b is in
  *   slot p % page of page table[b][p / page].  A position past the table or
  *   an entry outside 0 .. pages - 1 has no slot.
+ *   max_pages < 2^20, pages < 2^31, pages H page D <= 2^44.
  * Streams may share pages that are only read.
  *
  * kv4_append encodes k, v bf16 [B T][ldk], [B T][ldv] (token t of stream b in
@@ -475,7 +476,7 @@ int qk_norm_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int6
  *   the last query row stands at position lens[b] - 1 and a row sees no
  *   position after its own.  A row that sees nothing gives zeros.  Slots
  *   that are not seen may hold any bytes.
- *   D 64 or 128; Hq a multiple of H; scale > 0; B Lq Hq < 2^26.
+ *   D 64 or 128; Hq a multiple of H; scale > 0; B Lq Hq < 2^24.
  *   ws: with attn_kv4_workspace() bytes a call with few query rows splits
  *   the keys over more workgroups; less (also none) splits less.  The sums
  *   are made in an order that the sizes and ws_bytes decide.
@@ -505,7 +506,7 @@ int attn_kv4(const uint16_t* q, int64_t ldq, int64_t B, int64_t Lq, int Hq, int 
  * row of sequence b sees the states j < k_lens[b] (int32 [B]; NULL: Lk;
  * clamped to Lk) with mask[b][j] != 0 (u8 [B][Lk]; NULL: all).  States that
  * are not seen may hold any bits, NaN included.  A row that sees none gives
- * zeros.  D 64 or 128; Hq a multiple of Hkv; scale > 0; B Lq Hq < 2^26,
+ * zeros.  D 64 or 128; Hq a multiple of Hkv; scale > 0; B Lq Hq < 2^24,
  * B Lk < 2^26.  ws as for attn_kv4. */
 size_t attn_cross_workspace(int64_t B, int64_t Lq, int64_t Lk, int Hq, int Hkv, int D);
 int attn_cross(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v,

@@ -18,7 +18,8 @@ ROOT = os.path.dirname(HERE)
 OBJ_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["act_quant.hip", "qgemm.hip", "qgemm_i8.hip", "tdc.hip", "noalloc.hip", "convert_check.hip", "stage_ab.hip",
-           "qgemv.hip", "qk_norm.hip", "kv4.hip", "attn.hip", "abi.cpp"]
+           "qgemv.hip", "qk_norm.hip", "kv4.hip", "attn.hip", "attn_few.hip",
+           "abi.cpp"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -767,7 +767,7 @@ static int check_kv4(const Kv4Cache& c, int64_t B, int page) {
     return QA_ESHAPE;
   if (page < 16 || page > 1024 || (page & (page - 1))) return QA_ESHAPE;
   if (c.pages < 0 || c.max_pages < 0 || c.pages >= (int64_t)1 << 31 ||
-      c.max_pages >= (int64_t)1 << 27 || B < 0)
+      c.max_pages >= (int64_t)1 << 20 || B < 0)
     return QA_ESHAPE;
   if (c.pages > kMaxCache / ((int64_t)c.H * c.D * page)) return QA_ESHAPE;
   if (!aligned16(c.k_q) || !aligned16(c.k_s) || !aligned16(c.v_q) || !aligned16(c.v_s) ||
@@ -868,8 +868,8 @@ static int check_attn(const AttnArgs& a, const void* ws, size_t ws_bytes) {
   if (!(a.scale > 0.0f) || !std::isfinite(a.scale)) return QA_EINVAL;
   if (a.D != 64 && a.D != 128) return QA_ESHAPE;
   if (a.Hq <= 0 || a.Hkv <= 0 || a.Hq % a.Hkv || a.B < 0 || a.Lq < 0 ||
-      a.B >= (int64_t)1 << 24 || a.Lq >= (int64_t)1 << 26 || a.B * a.Lq >= (int64_t)1 << 26 ||
-      a.B * a.Lq * a.Hq >= (int64_t)1 << 26)
+      a.B >= (int64_t)1 << 24 || a.Lq >= (int64_t)1 << 24 || a.B * a.Lq >= (int64_t)1 << 24 ||
+      a.B * a.Lq * a.Hq >= (int64_t)1 << 24)
     return QA_ESHAPE;
   if (int s = check_heads(a.q, a.B * a.Lq, a.ldq, a.Hq, a.D)) return s;
   if (int s = check_heads(a.o, a.B * a.Lq, a.ldo, a.Hq, a.D)) return s;
@@ -883,8 +883,15 @@ static int check_attn(const AttnArgs& a, const void* ws, size_t ws_bytes) {
   return QA_OK;
 }
 
+// sizes that an attention call takes, with at least one row
+static bool attn_sizes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
+  return (D == 64 || D == 128) && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && B > 0 && Lq > 0 && L >= 0 &&
+         B < (int64_t)1 << 24 && Lq < (int64_t)1 << 24 && B * Lq < (int64_t)1 << 24 &&
+         B * Lq * Hq < (int64_t)1 << 24;
+}
+
 size_t attn_kv4_workspace(int64_t B, int64_t Lq, int Hq, int H, int D, int64_t max_len) {
-  return attn_ws_bytes(B, Lq, Hq, H, D, max_len);
+  return attn_sizes(B, Lq, Hq, H, D, max_len) ? attn_ws_bytes(B, Lq, Hq, H, D, max_len) : 0;
 }
 
 int attn_kv4(const uint16_t* q, int64_t ldq, int64_t B, int64_t Lq, int Hq, int H, int D,
@@ -915,7 +922,7 @@ int attn_kv4(const uint16_t* q, int64_t ldq, int64_t B, int64_t Lq, int Hq, int 
 }
 
 size_t attn_cross_workspace(int64_t B, int64_t Lq, int64_t Lk, int Hq, int Hkv, int D) {
-  return attn_ws_bytes(B, Lq, Hq, Hkv, D, Lk);
+  return attn_sizes(B, Lq, Hq, Hkv, D, Lk) ? attn_ws_bytes(B, Lq, Hq, Hkv, D, Lk) : 0;
 }
 
 int attn_cross(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v,
