@@ -181,7 +181,9 @@ struct CrossSource {
 template <bool F16, int N, class Most>
 __device__ __forceinline__ float query_operand(u32x4 (&q)[N], float scale_log2e, float k_scale,
                                                Most most) {
-  if constexpr (!F16) return scale_log2e;
+  // (at least the smallest normal number: a product of minus infinity, what
+  // is not seen, with it stays minus infinity)
+  if constexpr (!F16) return fmaxf(scale_log2e, 0x1p-126f);
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < N; ++i) top = max(top, fold_max(abs_max8_pk(q[i], u16x2{0, 0})));
@@ -194,7 +196,7 @@ __device__ __forceinline__ float query_operand(u32x4 (&q)[N], float scale_log2e,
     for (int j = 0; j < 4; ++j)
       q[i][j] = f16_pack(__builtin_ldexpf(bf16_lo(q[i][j]), -ex),
                          __builtin_ldexpf(bf16_hi(q[i][j]), -ex));
-  return __builtin_ldexpf(scale_log2e, ex) * k_scale;
+  return fmaxf(__builtin_ldexpf(scale_log2e, ex) * k_scale, 0x1p-126f);
 }
 
 // --------------------------------------------------------- split of the keys --
@@ -214,5 +216,9 @@ size_t attn_few_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t 
 template <class Source>
 hipError_t launch_attn_few(const AttnArgs& a, const Source& src, int64_t L, void* ws,
                            size_t ws_bytes, hipStream_t stream);
+
+// Many query rows (attn_tile.hip).
+template <class Source>
+hipError_t launch_attn_tile(const AttnArgs& a, const Source& src, hipStream_t stream);
 
 }  // namespace qact
