@@ -18,14 +18,14 @@ bool many(int64_t Lq, int Hq, int Hkv) { return Lq * (Hq / Hkv) >= kManyRows; }
 template <class Source>
 hipError_t launch(const AttnArgs& a, const Source& src, int64_t L, void* ws, size_t ws_bytes,
                   hipStream_t stream) {
-  if (many(a.Lq, a.Hq, a.Hkv)) return launch_attn_tile(a, src, stream);
+  if (many(a.Lq, a.Hq, a.Hkv)) return launch_attn_tile(a, src, L, ws, ws_bytes, stream);
   return launch_attn_few(a, src, L, ws, ws_bytes, stream);
 }
 
 }  // namespace
 
 size_t attn_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
-  if (many(Lq, Hq, Hkv)) return 0;
+  if (many(Lq, Hq, Hkv)) return attn_tile_ws_bytes(B, Lq, Hq, Hkv, D, L);
   return attn_few_ws_bytes(B, Lq, Hq, Hkv, D, L);
 }
 

@@ -60,6 +60,16 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
   return bf16_pack(a, b);
 }
 
+// acc + a pair's two elements, in float32
+template <bool F16>
+__device__ __forceinline__ float add_pair(uint32_t p, float acc) {
+  if constexpr (F16)
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, p), f16x2{(_Float16)1.0f, (_Float16)1.0f},
+                                  acc, false);
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, p),
+                                         bf16x2_t{(__bf16)1.0f, (__bf16)1.0f}, acc, false);
+}
+
 // Weights are stored as p 2^kPBias: in fp16 the largest is 2^15, so that
 // weights down to 2^-29 of it are normal numbers; in bf16 the range needs none.
 template <bool F16>
@@ -140,10 +150,32 @@ struct Kv4Source {
     const int n = lens[b];
     return n < 0 ? 0 : (n < cap ? n : (int)cap);
   }
-  // the page that holds positions j .. j + 15 (j % 16 == 0), -1: none
-  __device__ int page(int64_t b, int j) const {
-    const int32_t p = c.table[b * c.max_pages + (j >> c.page_log2)];
-    return p >= 0 && p < c.pages ? p : -1;
+  // The table's entries for the four sixteens of keys from `base` (base % 16
+  // == 0, n > 0 keys): scalar loads, looked at only when they are needed.
+  struct Pages {
+    int p[4];
+  };
+  __device__ __forceinline__ Pages pages(int64_t b, int base, int n) const {
+    typedef const __attribute__((address_space(4))) int32_t* scalar_ptr;
+    const scalar_ptr row = (scalar_ptr)(uintptr_t)(c.table + b * c.max_pages);
+    Pages r;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) r.p[t] = row[min(base + 16 * t, n - 1) >> c.page_log2];
+    return r;
+  }
+  // whether an entry names a page
+  __device__ __forceinline__ bool named(int p) const { return (uint64_t)(uint32_t)p < (uint64_t)c.pages; }
+  // Bit j: position base + j has a slot and lies before n.
+  __device__ __forceinline__ uint64_t seen(const Pages& pg, int base, int n) const {
+    uint64_t s = 0;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) s |= named(pg.p[t]) ? 0xFFFFull << (16 * t) : 0;
+    const int left = n - base;
+    return left >= 64 ? s : s & ((1ull << left) - 1);
+  }
+  // Row of position `at` (its page named) in a [pages][H][page] array.
+  __device__ __forceinline__ int64_t slot(int p, int hk, int at) const {
+    return (((int64_t)p * c.H + hk) << c.page_log2) + (at & ((1 << c.page_log2) - 1));
   }
   __device__ float k_scale() const { return *c.k_ts; }
   __device__ float v_scale() const { return *c.v_ts; }
@@ -159,6 +191,8 @@ struct CrossSource {
   const uint8_t* mask;
 
   static constexpr bool kF16 = false;
+  struct Pages {};
+  __device__ __forceinline__ Pages pages(int64_t, int, int) const { return {}; }
   static constexpr int causal = 0;
   __device__ int queries(int64_t, int64_t Lq) const { return (int)Lq; }
   __device__ int keys(int64_t b) const {
@@ -208,6 +242,19 @@ struct AttnSplit {
   float* m;       // [splits][rows] largest logit (log2 units), -inf: nothing seen
   float* l;       // [splits][rows]
   int64_t rows;
+
+  // `splits` partial results of `rows` rows laid out in a workspace
+  static AttnSplit in(void* ws, int64_t splits, int64_t rows, int D) {
+    AttnSplit s = {};
+    s.rows = rows;
+    if (splits > 1) {
+      s.o = static_cast<float*>(ws);
+      s.m = s.o + splits * rows * D;
+      s.l = s.m + splits * rows;
+    }
+    return s;
+  }
+  static size_t bytes(int64_t rows, int D) { return (size_t)rows * (D + 2) * 4; }
 };
 
 // Few query rows, the keys split over workgroups (attn_few.hip); L: the most
@@ -217,8 +264,15 @@ template <class Source>
 hipError_t launch_attn_few(const AttnArgs& a, const Source& src, int64_t L, void* ws,
                            size_t ws_bytes, hipStream_t stream);
 
-// Many query rows (attn_tile.hip).
+// Join `splits` partial results of every row.
 template <class Source>
-hipError_t launch_attn_tile(const AttnArgs& a, const Source& src, hipStream_t stream);
+hipError_t launch_attn_join(const AttnArgs& a, const Source& src, const AttnSplit& sp, int splits,
+                            hipStream_t stream);
+
+// Many query rows (attn_tile.hip).
+size_t attn_tile_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L);
+template <class Source>
+hipError_t launch_attn_tile(const AttnArgs& a, const Source& src, int64_t L, void* ws,
+                            size_t ws_bytes, hipStream_t stream);
 
 }  // namespace qact

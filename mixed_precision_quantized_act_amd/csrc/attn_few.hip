@@ -48,32 +48,22 @@ struct Few<Kv4Source, D> {
     uint64_t seen;
   };
 
-  // the four tiles' pages (uniform)
-  struct Pages {
-    int p[4];
-  };
-  static __device__ __forceinline__ Pages pages(const Kv4Source& s, int64_t b, int base, int n) {
-    Pages r;
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      r.p[t] = base + 16 * t < n ? __builtin_amdgcn_readfirstlane(s.page(b, base + 16 * t)) : -1;
-    return r;
-  }
-
-  static __device__ __forceinline__ void load(Regs& r, const Kv4Source& s, const Pages& pg,
-                                              int64_t, int hk, int base, int n, int lane) {
-    const int key = lane & 15, g = lane >> 4;
-    const int in_page = (1 << s.c.page_log2) - 1;
-    r.seen = 0;
+  static __device__ __forceinline__ void load(Regs& r, const Kv4Source& s,
+                                              const Kv4Source::Pages& pg, int64_t, int hk, int base,
+                                              int n, int lane) {
+    const uint32_t key = lane & 15, g = lane >> 4;
+    int64_t slot[4];
+    r.seen = s.seen(pg, base, n);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
+      slot[t] = -1;
 #pragma unroll
       for (int i = 0; i < kKWords; ++i) r.k[t][i] = 0;
       r.ks[t] = 0;
-      if (pg.p[t] < 0) continue;
-      const int64_t slot = (((int64_t)pg.p[t] * s.c.H + hk) << s.c.page_log2) + ((base + 16 * t) & in_page);
-      const uint8_t* kq = s.c.k_q + (slot + key) * (D / 2) + 4 * kKWords * g;
-      const uint8_t* ks = s.c.k_s + (slot + key) * kGroups + kKWords / 2 * g;
+      if (base + 16 * t >= n || !s.named(pg.p[t])) continue;
+      slot[t] = s.slot(pg.p[t], hk, base + 16 * t);
+      const uint8_t* kq = s.c.k_q + slot[t] * (D / 2) + (key * (D / 2) + 4 * kKWords * g);
+      const uint8_t* ks = s.c.k_s + slot[t] * kGroups + (key * kGroups + kKWords / 2 * g);
       if constexpr (D == 128) {
         const u32x4 w = *reinterpret_cast<const u32x4*>(kq);
 #pragma unroll
@@ -85,26 +75,23 @@ struct Few<Kv4Source, D> {
         r.k[t][1] = w[1];
         r.ks[t] = *ks;
       }
-      const int left = n - (base + 16 * t);
-      r.seen |= (left >= 16 ? 0xFFFFull : (1ull << left) - 1) << (16 * t);
     }
     // V codes: 16-byte vector x of the 64 keys is key x / (D/32)
 #pragma unroll
     for (int u = 0; u < kVLoads; ++u) {
       const int x = u * 64 + lane, vk = x / (D / 32);
       r.v[u] = u32x4{0, 0, 0, 0};
-      const int p = tile_page(pg, vk >> 4);
-      if (p >= 0) {
-        const int64_t slot = (((int64_t)p * s.c.H + hk) << s.c.page_log2) + ((base + vk) & in_page);
-        r.v[u] = *reinterpret_cast<const u32x4*>(s.c.v_q + slot * (D / 2) + 16 * (x % (D / 32)));
-      }
+      const int64_t lo = slot[(D == 128 ? u : 2 * u) % 4], hi = slot[(D == 128 ? u : 2 * u + 1) % 4];
+      const int64_t at = lane < 32 ? lo : hi;
+      if (at >= 0)
+        r.v[u] = *reinterpret_cast<const u32x4*>(s.c.v_q + (at + (vk & 15)) * (D / 2) + 16 * (x % (D / 32)));
     }
 #pragma unroll
     for (int i = 0; i < (kGroups + 3) / 4; ++i) r.vs[i] = 0;
-    const int p = tile_page(pg, lane >> 4);
-    if (p >= 0 && base + lane < n) {
-      const int64_t slot = (((int64_t)p * s.c.H + hk) << s.c.page_log2) + ((base + lane) & in_page);
-      const uint8_t* vs = s.c.v_s + slot * kGroups;
+    const int64_t s0 = slot[0], s1 = slot[1], s2 = slot[2], s3 = slot[3];
+    const int64_t at = g < 2 ? (g == 0 ? s0 : s1) : (g == 2 ? s2 : s3);
+    if (at >= 0 && base + lane < n) {
+      const uint8_t* vs = s.c.v_s + (at + key) * kGroups;
       if constexpr (D == 128) {
         const u32x2 w = *reinterpret_cast<const u32x2*>(vs);
         r.vs[0] = w[0];
@@ -113,9 +100,6 @@ struct Few<Kv4Source, D> {
         r.vs[0] = *reinterpret_cast<const uint32_t*>(vs);
       }
     }
-  }
-  static __device__ __forceinline__ int tile_page(const Pages& pg, int t) {
-    return t == 0 ? pg.p[0] : t == 1 ? pg.p[1] : t == 2 ? pg.p[2] : pg.p[3];
   }
 
   // element of the query operand's piece i, lane group g
@@ -194,11 +178,8 @@ struct Few<CrossSource, D> {
     u32x4 v[kVLoads];
     uint64_t seen;
   };
-  struct Pages {};
-  static __device__ __forceinline__ Pages pages(const CrossSource&, int64_t, int, int) { return {}; }
-
-  static __device__ __forceinline__ void load(Regs& r, const CrossSource& s, const Pages&,
-                                              int64_t b, int hk, int base, int n, int lane) {
+  static __device__ __forceinline__ void load(Regs& r, const CrossSource& s,
+                                              const CrossSource::Pages&, int64_t b, int hk, int base, int n, int lane) {
     const int key = lane & 15, g = lane >> 4;
     const int64_t row0 = b * s.Lk + base;
     bool on = base + lane < n;
@@ -307,9 +288,12 @@ attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gat
   float m = -INFINITY, l = 0.0f;                 // m: largest product, before the scale
 
   typename F::Regs cur;
-  typename F::Pages pg = F::pages(src, b, (c0 + wave) * kFewKeys, n);
-  if (c0 + wave < c1) F::load(cur, src, pg, b, hk, (c0 + wave) * kFewKeys, n, lane);
-  pg = F::pages(src, b, (c0 + wave + kFewWaves) * kFewKeys, n);
+  typename Source::Pages pg = {};
+  if (c0 + wave < c1) {
+    pg = src.pages(b, (c0 + wave) * kFewKeys, n);
+    F::load(cur, src, pg, b, hk, (c0 + wave) * kFewKeys, n, lane);
+    pg = src.pages(b, (c0 + wave + kFewWaves) * kFewKeys, n);
+  }
   for (int ch = c0 + wave; ch < c1; ch += kFewWaves) {
     const int base = ch * kFewKeys;
     f32x4 s[4];
@@ -326,19 +310,16 @@ attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gat
     // the next step's loads, and the pages of the one after
     if (ch + kFewWaves < c1) {
       F::load(cur, src, pg, b, hk, base + kFewWaves * kFewKeys, n, lane);
-      pg = F::pages(src, b, base + 2 * kFewWaves * kFewKeys, n);
+      pg = src.pages(b, base + 2 * kFewWaves * kFewKeys, n);
     }
     const bool whole = seen == ~0ull && base + kFewKeys <= all;
-    uint32_t bits = 0xFFFFu;                     // this lane's 16 keys, 4 t + r
     if (!whole) {
-      bits = 0;
 #pragma unroll
       for (int t4 = 0; t4 < 4; ++t4)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int key = 16 * t4 + 4 * g + r;
           const bool on = ((seen >> key) & 1) && base + key < upto;
-          bits |= (uint32_t)on << (4 * t4 + r);
           s[t4][r] = on ? s[t4][r] : -INFINITY;
         }
     }
@@ -359,11 +340,13 @@ attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gat
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t4][r], c, shift));
-        if (!whole) e[r] = (bits >> (4 * t4 + r)) & 1 ? e[r] : 0.0f;
-        l += e[r];
       }
-      p[t4 >> 1][2 * (t4 & 1)] = pack16<kF16>(e[0], e[1]);
-      p[t4 >> 1][2 * (t4 & 1) + 1] = pack16<kF16>(e[2], e[3]);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t w = pack16<kF16>(e[2 * r], e[2 * r + 1]);
+        l = add_pair<kF16>(w, l);
+        p[t4 >> 1][2 * (t4 & 1) + r] = w;
+      }
     }
     wave_lds_order();
 #pragma unroll
@@ -485,13 +468,11 @@ int64_t splits_of(int64_t B, int64_t Lq, int Hq, int Hkv, int64_t L) {
   return s < 1 ? 1 : s;
 }
 
-size_t split_bytes(int64_t rows, int D) { return (size_t)rows * (D + 2) * 4; }
-
 }  // namespace
 
 size_t attn_few_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
   const int64_t s = splits_of(B, Lq, Hq, Hkv, L);
-  return s > 1 ? s * split_bytes(B * Lq * Hq, D) : 0;
+  return s > 1 ? s * AttnSplit::bytes(B * Lq * Hq, D) : 0;
 }
 
 template <class Source>
@@ -499,15 +480,9 @@ hipError_t launch_attn_few(const AttnArgs& a, const Source& src, int64_t L, void
                            size_t ws_bytes, hipStream_t stream) {
   const int64_t rows = a.B * a.Lq * a.Hq;
   int64_t s = splits_of(a.B, a.Lq, a.Hq, a.Hkv, L);
-  const int64_t fit = (int64_t)(ws_bytes / split_bytes(rows, a.D));
+  const int64_t fit = (int64_t)(ws_bytes / AttnSplit::bytes(rows, a.D));
   if (s > fit) s = fit > 1 ? fit : 1;
-  AttnSplit sp = {};
-  sp.rows = rows;
-  if (s > 1) {
-    sp.o = static_cast<float*>(ws);
-    sp.m = sp.o + s * rows * a.D;
-    sp.l = sp.m + s * rows;
-  }
+  const AttnSplit sp = AttnSplit::in(ws, s, rows, a.D);
   const int64_t tiles = (a.Lq * (a.Hq / a.Hkv) + kFewRows - 1) / kFewRows;
   const Gate gt = current_gate();
   const dim3 grid((unsigned)(a.B * a.Hkv * tiles * s));
@@ -519,16 +494,26 @@ hipError_t launch_attn_few(const AttnArgs& a, const Source& src, int64_t L, void
                        src, sp, (int)tiles, (int)s, gt);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || s == 1) return e;
-  const dim3 jgrid((unsigned)((rows + 3) / 4));
+  return launch_attn_join(a, src, sp, (int)s, stream);
+}
+
+template <class Source>
+hipError_t launch_attn_join(const AttnArgs& a, const Source& src, const AttnSplit& sp, int splits,
+                            hipStream_t stream) {
+  const dim3 grid((unsigned)((sp.rows + 3) / 4));
   if (a.D == 64)
-    hipLaunchKernelGGL((attn_join_kernel<Source, 64>), jgrid, dim3(256), 0, stream, a, src, sp,
-                       (int)s, gt);
+    hipLaunchKernelGGL((attn_join_kernel<Source, 64>), grid, dim3(256), 0, stream, a, src, sp,
+                       splits, current_gate());
   else
-    hipLaunchKernelGGL((attn_join_kernel<Source, 128>), jgrid, dim3(256), 0, stream, a, src, sp,
-                       (int)s, gt);
+    hipLaunchKernelGGL((attn_join_kernel<Source, 128>), grid, dim3(256), 0, stream, a, src, sp,
+                       splits, current_gate());
   return hipGetLastError();
 }
 
+template hipError_t launch_attn_join(const AttnArgs&, const Kv4Source&, const AttnSplit&, int,
+                                     hipStream_t);
+template hipError_t launch_attn_join(const AttnArgs&, const CrossSource&, const AttnSplit&, int,
+                                     hipStream_t);
 template hipError_t launch_attn_few(const AttnArgs&, const Kv4Source&, int64_t, void*, size_t,
                                     hipStream_t);
 template hipError_t launch_attn_few(const AttnArgs&, const CrossSource&, int64_t, void*, size_t,

@@ -48,43 +48,30 @@ struct Tile<Kv4Source, D, T> {
   static constexpr int kUnits = kTileKeys * kGroups;
   static constexpr int kPer = 2 * kUnits / T;
 
-  // the pages of the tile's four sixteens of keys (uniform; -1: not seen)
-  struct Pages {
-    int p[4];
-  };
   struct Regs {
     u32x2 w[kPer];
     uint32_t s[kPer];              // group scale (0: not seen)
     uint64_t seen;
   };
-  static __device__ __forceinline__ Pages pages(const Kv4Source& s, int64_t b, int base, int n) {
-    Pages r;
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      r.p[t] = base + 16 * t < n ? __builtin_amdgcn_readfirstlane(s.page(b, base + 16 * t)) : -1;
-    return r;
-  }
-  static __device__ __forceinline__ void load(Regs& r, const Kv4Source& s, const Pages& pg,
-                                              int64_t, int hk, int base, int n, int tid) {
-    r.seen = 0;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int left = n - (base + 16 * t);
-      if (pg.p[t] >= 0) r.seen |= (left >= 16 ? 0xFFFFull : (1ull << left) - 1) << (16 * t);
-    }
-    const int in_page = (1 << s.c.page_log2) - 1;
+  // (a wave's unit lies within one sixteen of keys: its place is uniform)
+  static __device__ __forceinline__ void load(Regs& r, const Kv4Source& s,
+                                              const Kv4Source::Pages& pg, int64_t, int hk, int base,
+                                              int n, int wave, int lane) {
+    r.seen = s.seen(pg, base, n);
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
-      const int x = u * T + tid;
+      const int x = u * T + 64 * wave;
       const bool val = x >= kUnits;
-      const int y = x & (kUnits - 1), key = y / kGroups, g = y % kGroups, t = key >> 4;
-      const int p = t == 0 ? pg.p[0] : t == 1 ? pg.p[1] : t == 2 ? pg.p[2] : pg.p[3];
+      const int y = x & (kUnits - 1), t = y / kGroups >> 4;
+      const int p0 = pg.p[0], p1 = pg.p[1], p2 = pg.p[2], p3 = pg.p[3];
+      const int p = t < 2 ? (t == 0 ? p0 : p1) : (t == 2 ? p2 : p3);
+      const uint32_t z = (uint32_t)(y + lane) & (16 * kGroups - 1);       // (key % 16, group)
       r.w[u] = u32x2{0, 0};
       r.s[u] = 0;
-      if (p >= 0 && base + key < n) {
-        const int64_t slot = (((int64_t)p * s.c.H + hk) << s.c.page_log2) + ((base + key) & in_page);
-        r.w[u] = *reinterpret_cast<const u32x2*>((val ? s.c.v_q : s.c.k_q) + slot * (D / 2) + 8 * g);
-        r.s[u] = (val ? s.c.v_s : s.c.k_s)[slot * kGroups + g];
+      if (s.named(p) && base + 16 * t + (int)(z / kGroups) < n) {
+        const int64_t at = s.slot(p, hk, base + 16 * t);
+        r.w[u] = *reinterpret_cast<const u32x2*>((val ? s.c.v_q : s.c.k_q) + at * (D / 2) + 8 * z);
+        r.s[u] = ((val ? s.c.v_s : s.c.k_s) + at * kGroups)[z];
       }
     }
   }
@@ -110,24 +97,22 @@ struct Tile<CrossSource, D, T> {
   static constexpr int kUnits = kTileKeys * kPieces;
   static constexpr int kPer = 2 * kUnits / T;
 
-  struct Pages {};
   struct Regs {
     u32x4 w[kPer];
     uint64_t seen;
   };
-  static __device__ __forceinline__ Pages pages(const CrossSource&, int64_t, int, int) { return {}; }
-  static __device__ __forceinline__ void load(Regs& r, const CrossSource& s, const Pages&,
-                                              int64_t b, int hk, int base, int n, int tid) {
+  static __device__ __forceinline__ void load(Regs& r, const CrossSource& s,
+                                              const CrossSource::Pages&, int64_t b, int hk,
+                                              int base, int n, int wave, int lane) {
     const int64_t row0 = b * s.Lk + base;
-    const int lane = tid & 63;
     bool on = base + lane < n;
     if (on && s.mask) on = s.mask[row0 + lane] != 0;
     r.seen = __ballot(on);
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
-      const int x = u * T + tid;
+      const int x = u * T + 64 * wave;
       const bool val = x >= kUnits;
-      const int y = x & (kUnits - 1), key = y / kPieces, c = y % kPieces;
+      const int y = (x & (kUnits - 1)) + lane, key = y / kPieces, c = y % kPieces;
       r.w[u] = u32x4{0, 0, 0, 0};
       if ((r.seen >> key) & 1)           // (what is not seen may hold NaN: zeros)
         r.w[u] = *reinterpret_cast<const u32x4*>(
@@ -215,14 +200,15 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Ga
     va[d] = v_piece<D>(4 * h + ((lane & 15) >> 2), 4 * d + 2 * ((lane >> 4) & 1)) + 8 * (lane & 3);
 
   typename T::Regs regs;
-  typename T::Pages pg = T::pages(src, b, c0 * kTileKeys, n);
+  typename Source::Pages pg = {};
   uint64_t seen = 0;
   if (c0 < c1) {
-    T::load(regs, src, pg, b, hk, c0 * kTileKeys, n, tid);
+    pg = src.pages(b, c0 * kTileKeys, n);
+    T::load(regs, src, pg, b, hk, c0 * kTileKeys, n, wave, lane);
     seen = regs.seen;
     T::store(regs, lds[0][0], lds[0][1], tid);
+    pg = src.pages(b, (c0 + 1) * kTileKeys, n);
   }
-  pg = T::pages(src, b, (c0 + 1) * kTileKeys, n);
   for (int ch = c0; ch < c1; ++ch) {
     const char* const kt = lds[(ch - c0) & 1][0];
     const char* const vt = lds[(ch - c0) & 1][1];
@@ -230,8 +216,8 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Ga
     __syncthreads();         // this tile is staged, and the one before it no longer read
     const bool more = ch + 1 < c1;
     if (more) {
-      T::load(regs, src, pg, b, hk, base + kTileKeys, n, tid);
-      pg = T::pages(src, b, base + 2 * kTileKeys, n);
+      T::load(regs, src, pg, b, hk, base + kTileKeys, n, wave, lane);
+      pg = src.pages(b, base + 2 * kTileKeys, n);
     }
     if (base < wend) {
       const bool whole = seen == ~0ull && base + kTileKeys <= all;
@@ -271,15 +257,14 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Ga
             for (int d = 0; d < D / 32; ++d) o[x][d] *= f;
           }
           const float shift = kTileBias<kF16> - (m[x] == -INFINITY ? 0.0f : m[x] * c[x]);
-          float part = 0.0f;
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
             const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][i], c[x], shift));
             const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][i + 1], c[x], shift));
-            part += e0 + e1;
-            p[x][i >> 3][(i & 7) >> 1] = pack16<kF16>(e0, e1);
+            const uint32_t e = pack16<kF16>(e0, e1);
+            l[x] = add_pair<kF16>(e, l[x]);
+            p[x][i >> 3][(i & 7) >> 1] = e;
           }
-          l[x] += part;
         }
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2)
@@ -345,32 +330,48 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Ga
   }
 }
 
+
+#ifndef TS
+#define TS 1
+#endif
+// rows of a workgroup
+int tile_rows(int D) { return D == 64 ? 256 : 128; }
+
+int64_t splits_of(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) { return TS; }
+
 }  // namespace
 
-#ifndef TNQ
-#define TNQ 1
-#define TW 8
-#endif
-template <class Source>
-hipError_t launch_attn_tile(const AttnArgs& a, const Source& src, hipStream_t stream) {
-  const Gate gt = current_gate();
-  const int64_t rows = a.Lq * (a.Hq / a.Hkv);
-  AttnSplit sp = {};
-  sp.rows = a.B * a.Lq * a.Hq;
-  const int splits = 1;
-  const int per = a.D == 64 ? 32 * TNQ * TW : 128;
-  const int64_t tiles = (rows + per - 1) / per;
-  const dim3 grid((unsigned)(a.B * a.Hkv * splits * tiles));
-  if (a.D == 64)
-    hipLaunchKernelGGL((attn_tile_kernel<Source, 64, TNQ, TW>), grid, dim3(64 * TW), 0, stream,
-                       a, src, sp, (int)tiles, splits, gt);
-  else
-    hipLaunchKernelGGL((attn_tile_kernel<Source, 128, 1, 4>), grid, dim3(256), 0, stream,
-                       a, src, sp, (int)tiles, splits, gt);
-  return hipGetLastError();
+size_t attn_tile_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
+  const int64_t s = splits_of(B, Lq, Hq, Hkv, D, L);
+  return s > 1 ? s * AttnSplit::bytes(B * Lq * Hq, D) : 0;
 }
 
-template hipError_t launch_attn_tile(const AttnArgs&, const Kv4Source&, hipStream_t);
-template hipError_t launch_attn_tile(const AttnArgs&, const CrossSource&, hipStream_t);
+template <class Source>
+hipError_t launch_attn_tile(const AttnArgs& a, const Source& src, int64_t L, void* ws,
+                            size_t ws_bytes, hipStream_t stream) {
+  const Gate gt = current_gate();
+  const int64_t rows = a.B * a.Lq * a.Hq;
+  int64_t s = splits_of(a.B, a.Lq, a.Hq, a.Hkv, a.D, L);
+  const int64_t fit = (int64_t)(ws_bytes / AttnSplit::bytes(rows, a.D));
+  if (s > fit) s = fit > 1 ? fit : 1;
+  const AttnSplit sp = AttnSplit::in(ws, s, rows, a.D);
+  const int per = tile_rows(a.D);
+  const int64_t tiles = (a.Lq * (a.Hq / a.Hkv) + per - 1) / per;
+  const dim3 grid((unsigned)(a.B * a.Hkv * s * tiles));
+  if (a.D == 64)
+    hipLaunchKernelGGL((attn_tile_kernel<Source, 64, 1, 8>), grid, dim3(512), 0, stream, a, src,
+                       sp, (int)tiles, (int)s, gt);
+  else
+    hipLaunchKernelGGL((attn_tile_kernel<Source, 128, 1, 4>), grid, dim3(256), 0, stream, a, src,
+                       sp, (int)tiles, (int)s, gt);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || s == 1) return e;
+  return launch_attn_join(a, src, sp, (int)s, stream);
+}
+
+template hipError_t launch_attn_tile(const AttnArgs&, const Kv4Source&, int64_t, void*, size_t,
+                                     hipStream_t);
+template hipError_t launch_attn_tile(const AttnArgs&, const CrossSource&, int64_t, void*, size_t,
+                                     hipStream_t);
 
 }  // namespace qact
