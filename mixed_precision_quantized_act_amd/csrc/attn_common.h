@@ -150,26 +150,34 @@ struct Kv4Source {
     const int n = lens[b];
     return n < 0 ? 0 : (n < cap ? n : (int)cap);
   }
-  // The table's entries for the four sixteens of keys from `base` (base % 16
-  // == 0, n > 0 keys): scalar loads, looked at only when they are needed.
-  struct Pages {
+  // What the loads of 64 keys need to know first, asked a step ahead: the
+  // table's entries for the four sixteens of keys from `base` (base % 16 == 0,
+  // n > 0 keys), scalar loads that are looked at only when they are needed.
+  struct Look {
     int p[4];
   };
-  __device__ __forceinline__ Pages pages(int64_t b, int base, int n) const {
+  __device__ __forceinline__ Look look(int64_t b, int base, int n, int) const {
     typedef const __attribute__((address_space(4))) int32_t* scalar_ptr;
     const scalar_ptr row = (scalar_ptr)(uintptr_t)(c.table + b * c.max_pages);
-    Pages r;
+    Look r;
+    if (c.page_log2 >= 6) {              // one page
+      const int p = row[(uint32_t)min(base, n - 1) >> c.page_log2];
+      return {p, p, p, p};
+    }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) r.p[t] = row[min(base + 16 * t, n - 1) >> c.page_log2];
+    for (int t = 0; t < 4; ++t) r.p[t] = row[(uint32_t)min(base + 16 * t, n - 1) >> c.page_log2];
     return r;
   }
-  // whether an entry names a page
-  __device__ __forceinline__ bool named(int p) const { return (uint64_t)(uint32_t)p < (uint64_t)c.pages; }
+  // whether an entry names a page (pages < 2^31)
+  __device__ __forceinline__ bool named(int p) const { return (uint32_t)p < (uint32_t)c.pages; }
   // Bit j: position base + j has a slot and lies before n.
-  __device__ __forceinline__ uint64_t seen(const Pages& pg, int base, int n) const {
-    uint64_t s = 0;
+  __device__ __forceinline__ uint64_t seen(const Look& pg, int base, int n, int) const {
+    uint64_t s = named(pg.p[0]) ? ~0ull : 0ull;
+    if (c.page_log2 < 6) {
+      s &= 0xFFFFull;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) s |= named(pg.p[t]) ? 0xFFFFull << (16 * t) : 0;
+      for (int t = 1; t < 4; ++t) s |= named(pg.p[t]) ? 0xFFFFull << (16 * t) : 0;
+    }
     const int left = n - base;
     return left >= 64 ? s : s & ((1ull << left) - 1);
   }
@@ -191,8 +199,18 @@ struct CrossSource {
   const uint8_t* mask;
 
   static constexpr bool kF16 = false;
-  struct Pages {};
-  __device__ __forceinline__ Pages pages(int64_t, int, int) const { return {}; }
+  // The mask's byte for state base + lane.
+  struct Look {
+    uint32_t on;
+  };
+  __device__ __forceinline__ Look look(int64_t b, int base, int n, int lane) const {
+    if (base + lane >= n) return {0u};
+    return {mask ? mask[b * Lk + base + lane] : 1u};
+  }
+  // Bit j: state base + j is seen (by every row).
+  __device__ __forceinline__ uint64_t seen(const Look& k, int, int, int) const {
+    return __ballot(k.on != 0);
+  }
   static constexpr int causal = 0;
   __device__ int queries(int64_t, int64_t Lq) const { return (int)Lq; }
   __device__ int keys(int64_t b) const {

@@ -49,11 +49,11 @@ struct Few<Kv4Source, D> {
   };
 
   static __device__ __forceinline__ void load(Regs& r, const Kv4Source& s,
-                                              const Kv4Source::Pages& pg, int64_t, int hk, int base,
+                                              const Kv4Source::Look& pg, int64_t, int hk, int base,
                                               int n, int lane) {
     const uint32_t key = lane & 15, g = lane >> 4;
     int64_t slot[4];
-    r.seen = s.seen(pg, base, n);
+    r.seen = s.seen(pg, base, n, lane);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       slot[t] = -1;
@@ -179,12 +179,10 @@ struct Few<CrossSource, D> {
     uint64_t seen;
   };
   static __device__ __forceinline__ void load(Regs& r, const CrossSource& s,
-                                              const CrossSource::Pages&, int64_t b, int hk, int base, int n, int lane) {
+                                              const CrossSource::Look& look, int64_t b, int hk, int base, int n, int lane) {
     const int key = lane & 15, g = lane >> 4;
     const int64_t row0 = b * s.Lk + base;
-    bool on = base + lane < n;
-    if (on && s.mask) on = s.mask[row0 + lane] != 0;
-    r.seen = __ballot(on);
+    r.seen = s.seen(look, base, n, lane);
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -288,11 +286,11 @@ attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gat
   float m = -INFINITY, l = 0.0f;                 // m: largest product, before the scale
 
   typename F::Regs cur;
-  typename Source::Pages pg = {};
+  typename Source::Look look = {};
   if (c0 + wave < c1) {
-    pg = src.pages(b, (c0 + wave) * kFewKeys, n);
-    F::load(cur, src, pg, b, hk, (c0 + wave) * kFewKeys, n, lane);
-    pg = src.pages(b, (c0 + wave + kFewWaves) * kFewKeys, n);
+    look = src.look(b, (c0 + wave) * kFewKeys, n, lane);
+    F::load(cur, src, look, b, hk, (c0 + wave) * kFewKeys, n, lane);
+    look = src.look(b, (c0 + wave + kFewWaves) * kFewKeys, n, lane);
   }
   for (int ch = c0 + wave; ch < c1; ch += kFewWaves) {
     const int base = ch * kFewKeys;
@@ -307,10 +305,10 @@ attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gat
     }
     F::stage_v(cur, vlds, lane);
     const uint64_t seen = cur.seen;
-    // the next step's loads, and the pages of the one after
+    // the next step's loads, and what those of the one after need
     if (ch + kFewWaves < c1) {
-      F::load(cur, src, pg, b, hk, base + kFewWaves * kFewKeys, n, lane);
-      pg = src.pages(b, base + 2 * kFewWaves * kFewKeys, n);
+      F::load(cur, src, look, b, hk, base + kFewWaves * kFewKeys, n, lane);
+      look = src.look(b, base + 2 * kFewWaves * kFewKeys, n, lane);
     }
     const bool whole = seen == ~0ull && base + kFewKeys <= all;
     if (!whole) {

@@ -4,13 +4,19 @@
 // NVFP4 tile is expanded once for all rows), one tile ahead of the one that
 // the MFMAs read.
 //
-// What bounds it is the softmax: for heads of 64 an element of S costs 16
-// cycles of a SIMD's MFMA and about 29 of its VALU, 16 of them the
-// exponential (a quarter-rate instruction).  So the VALU is left with as
-// little else as possible: the running maximum is moved only when a tile
-// exceeds it by 2^8 (the weights are at most 2^8 times the 2^kTileBias of the
-// reference, in range of fp16), which spares the rescaling of the sums; a
-// lane holds one query row, so a maximum needs one exchange between lanes.
+// What bounds it is the VALU: for heads of 64 the weights of 32 keys take about
+// 165 ns of a SIMD, the two products' MFMAs 121.  Both run at once only when ONE
+// wave's instructions alternate between them (an MFMA and up to 7 VALU
+// instructions: the time of the longer; the same from two waves: nearly the
+// sum), so a wave forms the weights of 32 keys while its MFMAs compute the
+// logits of the next 32 and the second product of the 32 before.
+//
+// For the same reason the VALU is left with as little else as possible: no
+// maximum is taken of most tiles.  The weights are formed to the reference that
+// the row has and summed, which has to be done anyway; only where a sum says
+// that a weight may have grown beyond 2^8 times the reference's are the maxima
+// taken and the weights formed again (in fp16, too, they stay in range).  A
+// lane holds one query row, so that costs one exchange between lanes.
 #include "attn_common.h"
 
 namespace qact {
@@ -18,9 +24,12 @@ namespace qact {
 namespace {
 
 constexpr int kTileKeys = 64;
-constexpr float kTileSlack = 8.0f;
+// A weight is p 2^kTileBias relative to the reference, which moves when the
+// weights of 32 keys sum to more than kTileMost (2^8 times a weight of 1).
 template <bool F16>
 constexpr float kTileBias = F16 ? 7.0f : 0.0f;
+template <bool F16>
+constexpr float kTileMost = F16 ? 32768.0f : 256.0f;
 
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
@@ -36,10 +45,27 @@ __device__ __forceinline__ int v_piece(int key, int c) {
   return key * (D * 2) + 32 * ((c >> 1) ^ (D == 128 ? key & 7 : (key >> 1) & 3)) + 16 * (c & 1);
 }
 
+// Before a row has seen a key: any logit plus this gives an infinite weight,
+// minus infinity (not seen) one of zero.
+constexpr float kNoReference = 0x1.fffffep127f;
+
+// How a row tile's keys are cut: n pieces, each `size` parts of `whole` and
+// the last one what is left.
+struct Pieces {
+  int n, size, whole;
+};
+
 // Staging by T threads: a thread takes units of K or of V, the same side for
 // a whole wave.
 template <class Source, int D, int T>
 struct Tile;
+
+__device__ __forceinline__ float row_max(const f32x16& s) {
+  float top = max3(s[0], s[1], s[2]);
+#pragma unroll
+  for (int i = 3; i < 15; i += 2) top = max3(top, s[i], s[i + 1]);
+  return pair_max(fmaxf(top, s[15]));
+}
 
 // NVFP4: a unit is a group of 16 elements.
 template <int D, int T>
@@ -51,17 +77,16 @@ struct Tile<Kv4Source, D, T> {
   struct Regs {
     u32x2 w[kPer];
     uint32_t s[kPer];              // group scale (0: not seen)
-    uint64_t seen;
   };
   // (a wave's unit lies within one sixteen of keys: its place is uniform)
+  template <bool V>
   static __device__ __forceinline__ void load(Regs& r, const Kv4Source& s,
-                                              const Kv4Source::Pages& pg, int64_t, int hk, int base,
-                                              int n, int wave, int lane) {
-    r.seen = s.seen(pg, base, n);
+                                              const Kv4Source::Look& pg, uint64_t, int64_t, int hk,
+                                              int base, int n, int wave, int lane) {
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const int x = u * T + 64 * wave;
-      const bool val = x >= kUnits;
+      if ((x >= kUnits) != V) continue;
       const int y = x & (kUnits - 1), t = y / kGroups >> 4;
       const int p0 = pg.p[0], p1 = pg.p[1], p2 = pg.p[2], p3 = pg.p[3];
       const int p = t < 2 ? (t == 0 ? p0 : p1) : (t == 2 ? p2 : p3);
@@ -70,21 +95,22 @@ struct Tile<Kv4Source, D, T> {
       r.s[u] = 0;
       if (s.named(p) && base + 16 * t + (int)(z / kGroups) < n) {
         const int64_t at = s.slot(p, hk, base + 16 * t);
-        r.w[u] = *reinterpret_cast<const u32x2*>((val ? s.c.v_q : s.c.k_q) + at * (D / 2) + 8 * z);
-        r.s[u] = ((val ? s.c.v_s : s.c.k_s) + at * kGroups)[z];
+        r.w[u] = *reinterpret_cast<const u32x2*>((V ? s.c.v_q : s.c.k_q) + at * (D / 2) + 8 * z);
+        r.s[u] = ((V ? s.c.v_s : s.c.k_s) + at * kGroups)[z];
       }
     }
   }
-  static __device__ __forceinline__ void store(const Regs& r, char* k, char* v, int tid) {
+  template <bool V>
+  static __device__ __forceinline__ void store(const Regs& r, char* to, int wave, int lane) {
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
-      const int x = u * T + tid;
-      const bool val = x >= kUnits;
-      const int y = x & (kUnits - 1), key = y / kGroups, g = y % kGroups;
+      const int x = u * T + 64 * wave;
+      if ((x >= kUnits) != V) continue;
+      const int y = (x & (kUnits - 1)) + lane, key = y / kGroups, g = y % kGroups;
       const f16x2 sc = scale_f16<0>(r.s[u]);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<u32x4*>(val ? v + v_piece<D>(key, 2 * g + h) : k + k_piece<D>(key, 2 * g + h)) =
+        *reinterpret_cast<u32x4*>(to + (V ? v_piece<D>(key, 2 * g + h) : k_piece<D>(key, 2 * g + h))) =
             codes_f16(r.w[u][h], sc);
     }
   }
@@ -99,95 +125,249 @@ struct Tile<CrossSource, D, T> {
 
   struct Regs {
     u32x4 w[kPer];
-    uint64_t seen;
   };
+  template <bool V>
   static __device__ __forceinline__ void load(Regs& r, const CrossSource& s,
-                                              const CrossSource::Pages&, int64_t b, int hk,
-                                              int base, int n, int wave, int lane) {
+                                              const CrossSource::Look&, uint64_t seen, int64_t b,
+                                              int hk, int base, int, int wave, int lane) {
     const int64_t row0 = b * s.Lk + base;
-    bool on = base + lane < n;
-    if (on && s.mask) on = s.mask[row0 + lane] != 0;
-    r.seen = __ballot(on);
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const int x = u * T + 64 * wave;
-      const bool val = x >= kUnits;
+      if ((x >= kUnits) != V) continue;
       const int y = (x & (kUnits - 1)) + lane, key = y / kPieces, c = y % kPieces;
       r.w[u] = u32x4{0, 0, 0, 0};
-      if ((r.seen >> key) & 1)           // (what is not seen may hold NaN: zeros)
+      if ((seen >> key) & 1)             // (what is not seen may hold NaN: zeros)
         r.w[u] = *reinterpret_cast<const u32x4*>(
-            (val ? s.v + (row0 + key) * s.ldv : s.k + (row0 + key) * s.ldk) + hk * D + 8 * c);
+            (V ? s.v + (row0 + key) * s.ldv : s.k + (row0 + key) * s.ldk) + hk * D + 8 * c);
     }
   }
-  static __device__ __forceinline__ void store(const Regs& r, char* k, char* v, int tid) {
+  template <bool V>
+  static __device__ __forceinline__ void store(const Regs& r, char* to, int wave, int lane) {
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
-      const int x = u * T + tid;
-      const bool val = x >= kUnits;
-      const int y = x & (kUnits - 1), key = y / kPieces, c = y % kPieces;
-      *reinterpret_cast<u32x4*>(val ? v + v_piece<D>(key, c) : k + k_piece<D>(key, c)) = r.w[u];
+      const int x = u * T + 64 * wave;
+      if ((x >= kUnits) != V) continue;
+      const int y = (x & (kUnits - 1)) + lane, key = y / kPieces, c = y % kPieces;
+      *reinterpret_cast<u32x4*>(to + (V ? v_piece<D>(key, c) : k_piece<D>(key, c))) = r.w[u];
     }
   }
 };
 
-// Workgroup: (stream, key head, split, row tile), the row tile running
-// fastest.  W waves of NQ groups of 32 rows each.
-template <class Source, int D, int NQ, int W>
-__global__ void __launch_bounds__(64 * W, NQ == 1 && D == 64 ? 4 : 2)
-attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gate gate) {
+// One wave's rows: 32, a lane's row is its column of S^T (both halves of the
+// wave hold it, each half its keys).
+template <bool F16, int D>
+struct Rows {
+  u32x4 q[D / 16];
+  f32x16 o[D / 32];
+  u32x4 ones;                       // see sums()
+  float c, m, l, shift;
+
+  // Sum of a row's weights of 32 keys, on the MFMA: 16x16x32 takes the
+  // weights' registers as 16 columns and four groups of k, lanes l and l + 32
+  // (l + 16 and l + 48) being the two halves of row l % 16 (of row 16 + l % 16).
+  // Rows 0 and 8 of `ones` pick groups 0 and 2, rows 4 and 12 groups 1 and 3,
+  // so that every lane's first result is its own row's sum.  (On the VALU the
+  // sum costs 30 to 45 ns a step, here 10.)  A weight that is infinite or NaN
+  // makes the sums of rows l and l + 16 NaN: settle() sums those itself.
+  __device__ __forceinline__ void set_ones(int lane) {
+    const int row = lane & 15, g = lane >> 4;
+    const uint32_t w = (row & 3) == 0 && ((row >> 2) & 1) == (g & 1) ? (F16 ? 0x3C003C00u : 0x3F803F80u) : 0u;
+    ones = u32x4{w, w, w, w};
+  }
+
+  // The weights p of 32 keys whose logits are s, formed to the present
+  // reference, are about to be used: if one may be too large for some row, move
+  // the rows' references to their maxima and form them again.
+  __device__ __forceinline__ void settle(const f32x16& s, u32x4 (&p)[2], float sum) {
+    if (__builtin_amdgcn_ballot_w64(!(sum <= kTileMost<F16>))) {
+      const float mn = fmaxf(m, row_max(s));
+      const float ref = mn == -INFINITY ? 0.0f : mn;
+      const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - ref) * c);
+      m = mn;
+      shift = mn == -INFINITY ? kNoReference : kTileBias<F16> - ref * c;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) o[d] *= f;
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i], c, shift));
+        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i + 1], c, shift));
+        p[i >> 2][i & 3] = pack16<F16>(e0, e1);
+        sum += e0 + e1;
+      }
+      sum = pair_sum(sum);
+    }
+    l += sum;
+  }
+
+  // Step: settle the weights p (formed from `next`, their sum in `sum`); then
+  // the logits of 32 keys (K at k + ka, into `next`) and the second product of
+  // p (V at v + va) alternate with the weights of s, which go to pn and `sum`.
+  template <int KO, int VO>
+  __device__ __forceinline__ void step(const f32x16& s, u32x4 (&pn)[2], f32x16& next,
+                                       u32x4 (&p)[2], float& sum, const char* k,
+                                       const int (&ka)[D / 16], const char* v,
+                                       const int (&va)[D / 32]) {
+    constexpr int kN = 2 * (D / 16);            // products, of the two kinds in turn
+    constexpr int kAhead = 4;                   // operands read ahead
+    u32x4 f[kN];
+    auto fetch = [&](int g) {
+      f[g] = g & 1 ? v_operand<VO>(v, va, g / 2 / (D / 32), g / 2 % (D / 32))
+                   : *reinterpret_cast<const u32x4*>(k + KO + ka[g / 2]);
+    };
+#pragma unroll
+    for (int g = 0; g < kAhead; ++g) fetch(g);
+    settle(next, p, sum);
+    next = f32x16{};
+    // the weights of pair i in stages, one a turn, so that no instruction waits
+    // for the one before it
+    float x[16];
+    f32x4 total = {0, 0, 0, 0};
+    x[0] = __builtin_fmaf(s[0], c, shift);
+    x[1] = __builtin_fmaf(s[1], c, shift);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int g = i * kN / 8; g < (i + 1) * kN / 8; ++g) {
+        if (g + kAhead < kN) fetch(g + kAhead);
+        if (g & 1)
+          o[g / 2 % (D / 32)] = mfma32<F16>(f[g], p[g / 2 / (D / 32)], o[g / 2 % (D / 32)]);
+        else
+          next = mfma32<F16>(f[g], q[g / 2], next);
+      }
+      if (i == 5) total = mfma16<F16>(ones, pn[0], total);
+      if (i > 0) pn[(i - 1) >> 2][(i - 1) & 3] = pack16<F16>(x[2 * i - 2], x[2 * i - 1]);
+      x[2 * i] = __builtin_amdgcn_exp2f(x[2 * i]);
+      x[2 * i + 1] = __builtin_amdgcn_exp2f(x[2 * i + 1]);
+      if (i < 7) {
+        x[2 * i + 2] = __builtin_fmaf(s[2 * i + 2], c, shift);
+        x[2 * i + 3] = __builtin_fmaf(s[2 * i + 3], c, shift);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    pn[1][3] = pack16<F16>(x[14], x[15]);
+    sum = mfma16<F16>(ones, pn[1], total)[0];
+  }
+  // V^T of 16 keys s16 and elements 32 d .. as the second product's operand
+  template <int VO>
+  static __device__ __forceinline__ u32x4 v_operand(const char* v, const int (&va)[D / 32], int s16,
+                                                    int d) {
+    u32x4 r;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const s16x4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s16x4*)(v + va[d] + VO + (16 * s16 + 8 * j) * (D * 2)));
+      const u32x2 pr = __builtin_bit_cast(u32x2, w);
+      r[2 * j] = pr[0];
+      r[2 * j + 1] = pr[1];
+    }
+    return r;
+  }
+  __device__ __forceinline__ void logits(f32x16& next, const char* k, const int (&ka)[D / 16]) {
+    next = f32x16{};
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+      next = mfma32<F16>(*reinterpret_cast<const u32x4*>(k + ka[i]), q[i], next);
+  }
+  template <int VO>
+  __device__ __forceinline__ void second(const f32x16& s, u32x4 (&p)[2], float sum, const char* v,
+                                         const int (&va)[D / 32]) {
+    settle(s, p, sum);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+      o[i % (D / 32)] = mfma32<F16>(v_operand<VO>(v, va, i / (D / 32), i % (D / 32)),
+                                    p[i / (D / 32)], o[i % (D / 32)]);
+  }
+};
+
+// What is not seen of 32 keys: minus infinity.  `seen` from the first of
+// them; left: keys that this lane's row sees from there on.
+__device__ __forceinline__ void hide(f32x16& s, uint32_t seen, int left, int h) {
+  left -= 4 * h;
+  uint32_t bits = seen >> (4 * h);
+  bits &= left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)      // element i is key 8 (i / 4) + 4 h + i % 4
+    s[i] = bits & (1u << (8 * (i >> 2) + (i & 3))) ? s[i] : -INFINITY;
+}
+
+// Workgroup: (piece of the keys, stream, key head, row tile), the row tile
+// running fastest.  W waves of 32 rows each.
+//
+// Tile t is computed in two steps of 32 keys, each with the logits of the
+// step after it and the second product of the step before it, so K is needed
+// one step before V of the same keys and V one step after: K of tile t + 1 is
+// written to shared memory in the first step of tile t, before the only
+// barrier, V in the second.
+template <class Source, int D, int W>
+__global__ void __launch_bounds__(64 * W, 2)
+attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, Pieces pc, Gate gate) {
   if (gated_off(gate)) return;
   using T = Tile<Source, D, 64 * W>;
   constexpr bool kF16 = Source::kF16;
-  constexpr int kBytes = kTileKeys * D * 2;
-  __shared__ __align__(16) char lds[2][2][kBytes];
+  constexpr int kBytes = kTileKeys * D * 2, kHalf = kBytes / 2;
+  __shared__ __align__(16) char kt[2 * kBytes];            // two tiles
+  __shared__ __align__(16) char vt[2 * kBytes];
 
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tile = blockIdx.x % tiles;
-  const int at = blockIdx.x / tiles, split = at % splits;
-  const int hk = at / splits % a.Hkv;
-  const int64_t b = at / splits / a.Hkv;
+  const int at = blockIdx.x / tiles, hk = at % a.Hkv;
+  const int bs = at / a.Hkv, piece = bs / (int)a.B;
+  const int64_t b = bs - piece * (int)a.B;
   const int G = a.Hq / a.Hkv;
   const int nq = src.queries(b, a.Lq), n = src.keys(b);
   const int rows = nq * G;
-  constexpr int kRows = 32 * NQ * W;
-  if (tile * kRows >= rows) return;
-  const int row0 = tile * kRows + wave * 32 * NQ;         // the wave's first row
-  const int wlast = min(row0 + 32 * NQ, rows) - 1;        // and last (before row0: it has none)
+  if (tile * (32 * W) >= rows) return;
+  const int row0 = tile * (32 * W) + wave * 32;           // the wave's first row
+  const int wlast = min(row0 + 32, rows) - 1;             // and last (before row0: it has none)
 
   // keys that every row of the wave sees, that any row of it and of the
   // workgroup sees
   const int all = src.causal ? n - (nq - 1 - row0 / G) : n;
   const int wend = wlast < row0 ? 0 : (src.causal ? n - (nq - 1 - wlast / G) : n);
-  const int last = min(tile * kRows + kRows, rows) - 1;
+  const int last = min(tile * (32 * W) + 32 * W, rows) - 1;
   const int end = src.causal ? n - (nq - 1 - last / G) : n;
   const int chunks = (max(end, 0) + kTileKeys - 1) / kTileKeys;
-  const int c0 = (int)((int64_t)chunks * split / splits);
-  const int c1 = (int)((int64_t)chunks * (split + 1) / splits);
+  const int c0 = (int)((int64_t)chunks * (piece * pc.size) / pc.whole);
+  const int c1 = (int)((int64_t)chunks * min(piece * pc.size + pc.size, pc.whole) / pc.whole);
+  const int base0 = c0 * kTileKeys, nt = c1 - c0;
+  // tiles of which this wave's rows see anything
+  const int mine = min(nt, max(0, (wend - base0 + kTileKeys - 1) / kTileKeys));
 
-  u32x4 q[NQ][D / 16];
-  float c[NQ], m[NQ], l[NQ];
-  int upto[NQ];
-  f32x16 o[NQ][D / 32];
-#pragma unroll
-  for (int x = 0; x < NQ; ++x) {
-    const int row = row0 + 32 * x + col, t = row / G;
-    upto[x] = src.causal ? n - (nq - 1 - t) : n;
-    const uint16_t* p = a.q + (b * a.Lq + t) * a.ldq + (int64_t)(hk * G + row - t * G) * D + 8 * h;
+  typename T::Regs regs = {};
+  typename Source::Look look = {};
+  uint64_t seen = 0, seen_next = 0;
+  if (nt > 0) {
+    look = src.look(b, base0, n, lane);
+    seen = src.seen(look, base0, n, lane);
+    T::template load<false>(regs, src, look, seen, b, hk, base0, n, wave, lane);
+    T::template load<true>(regs, src, look, seen, b, hk, base0, n, wave, lane);
+    look = src.look(b, base0 + kTileKeys, n, lane);
+  }
+
+  const int row = row0 + col, t = row / G;
+  const int upto = src.causal ? n - (nq - 1 - t) : n;
+  const int head = hk * G + row - t * G;
+  Rows<kF16, D> r;
+  {
+    const uint16_t* p = a.q + (b * a.Lq + t) * a.ldq + (int64_t)head * D + 8 * h;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      q[x][i] = u32x4{0, 0, 0, 0};
-      if (row < rows) q[x][i] = *reinterpret_cast<const u32x4*>(p + 16 * i);
+      r.q[i] = u32x4{0, 0, 0, 0};
+      if (row < rows) r.q[i] = *reinterpret_cast<const u32x4*>(p + 16 * i);
     }
-    c[x] = query_operand<kF16>(q[x], a.scale * kLog2e, src.k_scale(),
-                               [](float v) { return pair_max(v); });
-    m[x] = -INFINITY;
-    l[x] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[x][d][i] = 0.0f;
   }
+  r.c = query_operand<kF16>(r.q, a.scale * kLog2e, src.k_scale(),
+                            [](float v) { return pair_max(v); });
+  r.m = -INFINITY;
+  r.shift = kNoReference;
+  r.l = 0.0f;
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d) r.o[d] = f32x16{};
+  r.set_ones(lane);
 
   // this lane's places in a staged tile: K of key `col`, piece 2 i + h (keys
   // 32 further on: the same exchange of pieces); V of keys 4 h + lane % 16 / 4
@@ -199,151 +379,146 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Ga
   for (int d = 0; d < D / 32; ++d)
     va[d] = v_piece<D>(4 * h + ((lane & 15) >> 2), 4 * d + 2 * ((lane >> 4) & 1)) + 8 * (lane & 3);
 
-  typename T::Regs regs;
-  typename Source::Pages pg = {};
-  uint64_t seen = 0;
-  if (c0 < c1) {
-    pg = src.pages(b, c0 * kTileKeys, n);
-    T::load(regs, src, pg, b, hk, c0 * kTileKeys, n, wave, lane);
-    seen = regs.seen;
-    T::store(regs, lds[0][0], lds[0][1], tid);
-    pg = src.pages(b, (c0 + 1) * kTileKeys, n);
+  f32x16 s0 = {}, s1 = {};
+  u32x4 p0[2] = {}, p1[2] = {};
+  float sum = 0.0f;
+  if (nt > 0) {
+    T::template store<false>(regs, kt, wave, lane);
+    T::template store<true>(regs, vt, wave, lane);
+    __syncthreads();
+    if (mine > 0) r.logits(s0, kt, ka);
   }
-  for (int ch = c0; ch < c1; ++ch) {
-    const char* const kt = lds[(ch - c0) & 1][0];
-    const char* const vt = lds[(ch - c0) & 1][1];
-    const int base = ch * kTileKeys;
-    __syncthreads();         // this tile is staged, and the one before it no longer read
-    const bool more = ch + 1 < c1;
-    if (more) {
-      T::load(regs, src, pg, b, hk, base + kTileKeys, n, wave, lane);
-      pg = src.pages(b, base + 2 * kTileKeys, n);
-    }
-    if (base < wend) {
-      const bool whole = seen == ~0ull && base + kTileKeys <= all;
-#pragma unroll 1
-      for (int k2 = 0; k2 < 2; ++k2) {
-        f32x16 s[NQ];
+  // the next tile's loads; V's are stored in the second step
+  auto fetch = [&](int base) {
+    seen_next = src.seen(look, base, n, lane);
+    T::template load<false>(regs, src, look, seen_next, b, hk, base, n, wave, lane);
+    T::template load<true>(regs, src, look, seen_next, b, hk, base, n, wave, lane);
+    look = src.look(b, base + kTileKeys, n, lane);
+  };
+  int i = 0;
+  for (; i < mine; ++i) {
+    const int base = base0 + i * kTileKeys, other = i & 1 ? 0 : kBytes;
+    const bool more = i + 1 < nt;
+    if (more) fetch(base + kTileKeys);
+    const bool whole = seen == ~0ull && base + kTileKeys <= all;
+    // `va` is at the tile before (in the first there is none: weights of zero
+    // on this tile's values), `ka` at this one
+    if (!whole) hide(s0, (uint32_t)seen, upto - base, h);
+    r.template step<kHalf, kHalf>(s0, p0, s1, p1, sum, kt, ka, vt, va);
+    if (more) T::template store<false>(regs, kt + other, wave, lane);
+    __syncthreads();
+    // on to the next tile of K (after the last: logits that nobody looks at)
+    // and to this one of V
+    const int ks = more ? (i & 1 ? -kBytes : kBytes) : 0, vs = i == 0 ? 0 : (i & 1 ? kBytes : -kBytes);
 #pragma unroll
-        for (int x = 0; x < NQ; ++x) s[x] = f32x16{};
+    for (int d = 0; d < D / 16; ++d) ka[d] += ks;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const u32x4 k = *reinterpret_cast<const u32x4*>(kt + ka[i] + 32 * k2 * (D * 2));
-#pragma unroll
-          for (int x = 0; x < NQ; ++x) s[x] = mfma32<kF16>(k, q[x][i], s[x]);
-        }
-        u32x4 p[NQ][2];
-#pragma unroll
-        for (int x = 0; x < NQ; ++x) {
-          if (!whole) {            // bit 8 (i / 4) + i % 4: this lane's element i is seen
-            const int left = upto[x] - (base + 32 * k2 + 4 * h);
-            uint32_t bits = (uint32_t)(seen >> (32 * k2)) >> (4 * h);
-            bits &= left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              s[x][i] = bits & (1u << (8 * (i >> 2) + (i & 3))) ? s[x][i] : -INFINITY;
-          }
-          float top = max3(s[x][0], s[x][1], s[x][2]);
-#pragma unroll
-          for (int i = 3; i < 15; i += 2) top = max3(top, s[x][i], s[x][i + 1]);
-          top = pair_max(fmaxf(top, s[x][15]));
-          // (no key seen yet: the difference is infinite; none at all: NaN, not greater)
-          if (__builtin_amdgcn_ballot_w64((top - m[x]) * c[x] > kTileSlack)) {
-            const float mn = fmaxf(m[x], top);
-            const float f = m[x] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m[x] - mn) * c[x]);
-            m[x] = mn;
-            l[x] *= f;
-#pragma unroll
-            for (int d = 0; d < D / 32; ++d) o[x][d] *= f;
-          }
-          const float shift = kTileBias<kF16> - (m[x] == -INFINITY ? 0.0f : m[x] * c[x]);
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][i], c[x], shift));
-            const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][i + 1], c[x], shift));
-            const uint32_t e = pack16<kF16>(e0, e1);
-            l[x] = add_pair<kF16>(e, l[x]);
-            p[x][i >> 3][(i & 7) >> 1] = e;
-          }
-        }
-#pragma unroll
-        for (int s2 = 0; s2 < 2; ++s2)
-#pragma unroll
-          for (int d = 0; d < D / 32; ++d) {
-            u32x4 v;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const s16x4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(
-                  vt + va[d] + (32 * k2 + 16 * s2 + 8 * j) * (D * 2)));
-              const u32x2 pr = __builtin_bit_cast(u32x2, w);
-              v[2 * j] = pr[0];
-              v[2 * j + 1] = pr[1];
-            }
-#pragma unroll
-            for (int x = 0; x < NQ; ++x) o[x][d] = mfma32<kF16>(v, p[x][s2], o[x][d]);
-          }
-      }
-    }
-    if (more) {
-      seen = regs.seen;
-      T::store(regs, lds[(ch + 1 - c0) & 1][0], lds[(ch + 1 - c0) & 1][1], tid);
-    }
+    for (int d = 0; d < D / 32; ++d) va[d] += vs;
+    if (!whole) hide(s1, (uint32_t)(seen >> 32), upto - base - 32, h);
+    r.template step<0, 0>(s1, p1, s0, p0, sum, kt, ka, vt, va);
+    if (more) T::template store<true>(regs, vt + other, wave, lane);
+    seen = seen_next;
+  }
+  if (mine > 0) r.template second<kHalf>(s1, p1, sum, vt, va);
+  // tiles that only other waves' rows see
+  for (; i < nt; ++i) {
+    const int base = base0 + i * kTileKeys, other = i & 1 ? 0 : kBytes;
+    const bool more = i + 1 < nt;
+    if (more) fetch(base + kTileKeys);
+    if (more) T::template store<false>(regs, kt + other, wave, lane);
+    __syncthreads();
+    if (more) T::template store<true>(regs, vt + other, wave, lane);
   }
 
+  const float lt = r.l;
+  if (pc.n == 1) {
+    const float f = lt == 0.0f ? 0.0f : src.v_scale() / lt;
+    uint16_t* dst = a.o + (b * a.Lq + t) * a.ldo + (int64_t)head * D;
 #pragma unroll
-  for (int x = 0; x < NQ; ++x) {
-    const float lt = pair_sum(l[x]);
-    const int row = row0 + 32 * x + col, t = row / G;
-    const int head = hk * G + row - t * G;
-    // (times zero, not left out: a sum that is NaN stays so)
-    if (splits == 1) {
-      const float f = lt == 0.0f ? 0.0f : src.v_scale() / lt;
-      uint16_t* dst = a.o + (b * a.Lq + t) * a.ldo + (int64_t)head * D;
+    for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; i += 8) {
-          // elements 8 (i / 4) + 4 h + 0..3 and 8 (i / 4 + 1) + 4 h + 0..3: lanes l and
-          // l + 32 exchange halves, so that each holds 8 consecutive ones
-          const auto w0 = __builtin_amdgcn_permlane32_swap(
-              bf16_pack(o[x][d][i] * f, o[x][d][i + 1] * f),
-              bf16_pack(o[x][d][i + 4] * f, o[x][d][i + 5] * f), false, false);
-          const auto w1 = __builtin_amdgcn_permlane32_swap(
-              bf16_pack(o[x][d][i + 2] * f, o[x][d][i + 3] * f),
-              bf16_pack(o[x][d][i + 6] * f, o[x][d][i + 7] * f), false, false);
-          if (row < rows)
-            *reinterpret_cast<u32x4*>(dst + 32 * d + 2 * i + 8 * h) = u32x4{w0[0], w1[0], w0[1], w1[1]};
-        }
-    } else if (row < rows) {
-      const int64_t to = (int64_t)split * sp.rows + (b * a.Lq + t) * a.Hq + head;
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<f32x4*>(sp.o + to * D + 32 * d + 2 * i + 4 * h) =
-              f32x4{o[x][d][i], o[x][d][i + 1], o[x][d][i + 2], o[x][d][i + 3]};
-      if (h == 0) {
-        sp.m[to] = m[x] == -INFINITY ? m[x] : m[x] * c[x];
-        sp.l[to] = lt;
+      for (int i = 0; i < 16; i += 8) {
+        // elements 8 (i / 4) + 4 h + 0..3 and 8 (i / 4 + 1) + 4 h + 0..3: lanes l and
+        // l + 32 exchange halves, so that each holds 8 consecutive ones
+        const auto w0 = __builtin_amdgcn_permlane32_swap(
+            bf16_pack(r.o[d][i] * f, r.o[d][i + 1] * f),
+            bf16_pack(r.o[d][i + 4] * f, r.o[d][i + 5] * f), false, false);
+        const auto w1 = __builtin_amdgcn_permlane32_swap(
+            bf16_pack(r.o[d][i + 2] * f, r.o[d][i + 3] * f),
+            bf16_pack(r.o[d][i + 6] * f, r.o[d][i + 7] * f), false, false);
+        if (row < rows)
+          *reinterpret_cast<u32x4*>(dst + 32 * d + 2 * i + 8 * h) = u32x4{w0[0], w1[0], w0[1], w1[1]};
       }
+  } else if (row < rows) {
+    const int64_t to = (int64_t)piece * sp.rows + (b * a.Lq + t) * a.Hq + head;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<f32x4*>(sp.o + to * D + 32 * d + 2 * i + 4 * h) =
+            f32x4{r.o[d][i], r.o[d][i + 1], r.o[d][i + 2], r.o[d][i + 3]};
+    if (h == 0) {
+      sp.m[to] = r.m == -INFINITY ? r.m : r.m * r.c;
+      sp.l[to] = lt;
     }
   }
 }
 
-
-#ifndef TS
-#define TS 1
-#endif
 // rows of a workgroup
-int tile_rows(int D) { return D == 64 ? 256 : 128; }
+constexpr int kTileRows = 256;
 
-int64_t splits_of(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) { return TS; }
+// Two workgroups fit a CU: this many run at once.  Row tiles that do not fill
+// them (or fill them badly) have their keys cut into pieces: S equal ones, or
+// as many large ones as fit at once and a small one for the places that are
+// left, which takes each of those several times.  The cost in units of a
+// tile's keys: the time of the slowest place, a workgroup alone on its CU
+// at 3/4 of the time; and for more than one piece the partial sums, written
+// and read again, and the launch that joins them.
+//   1350 rows x 30 heads of 64, 12376 keys (180 row tiles): 1 piece 305 us, 2
+//   254 us, 4 210 us (3 large and small: see the header).
+constexpr int64_t kPlaces = 256;
+
+Pieces pieces_of(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L, size_t ws_bytes) {
+  const int64_t rows = B * Lq * Hq;
+  const int64_t u = B * Hkv * ((Lq * (Hq / Hkv) + kTileRows - 1) / kTileRows);
+  const int64_t chunks = (L + kTileKeys - 1) / kTileKeys;
+  const double tau = D == 64 ? 2.0 : 4.0;                      // us a tile of keys
+  const int64_t fit = (int64_t)(ws_bytes / AttnSplit::bytes(rows, D));
+  Pieces best = {1, 1, 1};
+  double least = 0.0;
+  for (int n = 1; n <= 16; ++n) {
+    if (n > 1 && (n > fit || n > chunks)) break;
+    for (int uneven = 0; uneven < 2; ++uneven) {
+      Pieces p = {n, 1, n};
+      double span;                                              // of the slowest place, of `whole`
+      if (!uneven) {
+        const int64_t k = u * n;
+        const int64_t rest = k % kPlaces;
+        span = (double)(k / kPlaces) + (rest == 0 ? 0.0 : rest <= kPlaces / 2 ? 0.75 : 1.0);
+      } else {
+        const int64_t left = kPlaces - u * (n - 1);             // places beside the large pieces
+        if (n < 2 || left <= 0) continue;
+        p.size = (int)((u + left - 1) / left);
+        if (p.size < 2) continue;
+        p.whole = (n - 1) * p.size + 1;
+        span = p.size;
+      }
+      double cost = span / p.whole * (double)chunks * tau;
+      if (n > 1) cost += 4.0 + (double)n * (double)rows * D * 4 * 1.5 / 4e6;
+      if (n == 1 || cost < least) {
+        least = cost;
+        best = p;
+      }
+    }
+  }
+  return best;
+}
 
 }  // namespace
 
 size_t attn_tile_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
-  const int64_t s = splits_of(B, Lq, Hq, Hkv, D, L);
-  return s > 1 ? s * AttnSplit::bytes(B * Lq * Hq, D) : 0;
+  const Pieces p = pieces_of(B, Lq, Hq, Hkv, D, L, (size_t)1 << 40);
+  return p.n > 1 ? p.n * AttnSplit::bytes(B * Lq * Hq, D) : 0;
 }
 
 template <class Source>
@@ -351,22 +526,22 @@ hipError_t launch_attn_tile(const AttnArgs& a, const Source& src, int64_t L, voi
                             size_t ws_bytes, hipStream_t stream) {
   const Gate gt = current_gate();
   const int64_t rows = a.B * a.Lq * a.Hq;
-  int64_t s = splits_of(a.B, a.Lq, a.Hq, a.Hkv, a.D, L);
-  const int64_t fit = (int64_t)(ws_bytes / AttnSplit::bytes(rows, a.D));
-  if (s > fit) s = fit > 1 ? fit : 1;
-  const AttnSplit sp = AttnSplit::in(ws, s, rows, a.D);
-  const int per = tile_rows(a.D);
-  const int64_t tiles = (a.Lq * (a.Hq / a.Hkv) + per - 1) / per;
-  const dim3 grid((unsigned)(a.B * a.Hkv * s * tiles));
+  Pieces pc = pieces_of(a.B, a.Lq, a.Hq, a.Hkv, a.D, L, ws_bytes);
+#ifdef TS
+  if (TS * AttnSplit::bytes(rows, a.D) <= ws_bytes) pc = {TS, TSZ, TWH};
+#endif
+  const AttnSplit sp = AttnSplit::in(ws, pc.n, rows, a.D);
+  const int64_t tiles = (a.Lq * (a.Hq / a.Hkv) + kTileRows - 1) / kTileRows;
+  const dim3 grid((unsigned)(a.B * a.Hkv * pc.n * tiles));
   if (a.D == 64)
-    hipLaunchKernelGGL((attn_tile_kernel<Source, 64, 1, 8>), grid, dim3(512), 0, stream, a, src,
-                       sp, (int)tiles, (int)s, gt);
+    hipLaunchKernelGGL((attn_tile_kernel<Source, 64, 8>), grid, dim3(512), 0, stream, a, src,
+                       sp, (int)tiles, pc, gt);
   else
-    hipLaunchKernelGGL((attn_tile_kernel<Source, 128, 1, 4>), grid, dim3(256), 0, stream, a, src,
-                       sp, (int)tiles, (int)s, gt);
+    hipLaunchKernelGGL((attn_tile_kernel<Source, 128, 8>), grid, dim3(512), 0, stream, a, src,
+                       sp, (int)tiles, pc, gt);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || s == 1) return e;
-  return launch_attn_join(a, src, sp, (int)s, stream);
+  if (e != hipSuccess || pc.n == 1) return e;
+  return launch_attn_join(a, src, sp, pc.n, stream);
 }
 
 template hipError_t launch_attn_tile(const AttnArgs&, const Kv4Source&, int64_t, void*, size_t,
