@@ -146,40 +146,40 @@ struct Kv4Source {
     return n < 0 ? 0 : (n < Lq ? n : (int)Lq);
   }
   __device__ int keys(int64_t b) const {
-    const int64_t cap = c.max_pages << c.page_log2;
+    const int64_t cap = c.pages ? c.max_pages << c.page_log2 : 0;
     const int n = lens[b];
     return n < 0 ? 0 : (n < cap ? n : (int)cap);
   }
   // What the loads of 64 keys need to know first, asked a step ahead: the
   // table's entries for the four sixteens of keys from `base` (base % 16 == 0,
-  // n > 0 keys), scalar loads that are looked at only when they are needed.
+  // n > 0 keys), one in each of four lanes.  A vector load on purpose: a scalar
+  // one counts with the shared-memory operations but returns out of their
+  // order, so that every wait for one of those would wait for it too (measured: a
+  // quarter of the time).
   struct Look {
-    int p[4];
+    int e;
   };
-  __device__ __forceinline__ Look look(int64_t b, int base, int n, int) const {
-    typedef const __attribute__((address_space(4))) int32_t* scalar_ptr;
-    const scalar_ptr row = (scalar_ptr)(uintptr_t)(c.table + b * c.max_pages);
-    Look r;
-    if (c.page_log2 >= 6) {              // one page
-      const int p = row[(uint32_t)min(base, n - 1) >> c.page_log2];
-      return {p, p, p, p};
-    }
-#pragma unroll
-    for (int t = 0; t < 4; ++t) r.p[t] = row[(uint32_t)min(base + 16 * t, n - 1) >> c.page_log2];
-    return r;
+  __device__ __forceinline__ Look look(int64_t b, int base, int n, int lane) const {
+    const int at = min(base + 16 * (lane & 3), n - 1);
+    return {c.table[b * c.max_pages + ((uint32_t)at >> c.page_log2)]};
+  }
+  static __device__ __forceinline__ int entry(const Look& k, int t) {
+    return __builtin_amdgcn_readlane(k.e, t);
   }
   // whether an entry names a page (pages < 2^31)
   __device__ __forceinline__ bool named(int p) const { return (uint32_t)p < (uint32_t)c.pages; }
   // Bit j: position base + j has a slot and lies before n.
-  __device__ __forceinline__ uint64_t seen(const Look& pg, int base, int n, int) const {
-    uint64_t s = named(pg.p[0]) ? ~0ull : 0ull;
-    if (c.page_log2 < 6) {
-      s &= 0xFFFFull;
+  __device__ __forceinline__ uint64_t seen(const Look& k, int base, int n, int lane) const {
+    // (bit t of the ballot: sixteen t's entry)
+    const uint32_t ok = (uint32_t)__ballot(named(k.e)) & 15u;
+    uint64_t s = ~0ull;
+    if (ok != 15u) {
+      s = 0;
 #pragma unroll
-      for (int t = 1; t < 4; ++t) s |= named(pg.p[t]) ? 0xFFFFull << (16 * t) : 0;
+      for (int t = 0; t < 4; ++t) s |= (ok >> t) & 1 ? 0xFFFFull << (16 * t) : 0;
     }
     const int left = n - base;
-    return left >= 64 ? s : s & ((1ull << left) - 1);
+    return left >= 64 ? s : left <= 0 ? 0 : s & ((1ull << left) - 1);
   }
   // Row of position `at` (its page named) in a [pages][H][page] array.
   __device__ __forceinline__ int64_t slot(int p, int hk, int at) const {

@@ -60,8 +60,9 @@ struct Few<Kv4Source, D> {
 #pragma unroll
       for (int i = 0; i < kKWords; ++i) r.k[t][i] = 0;
       r.ks[t] = 0;
-      if (base + 16 * t >= n || !s.named(pg.p[t])) continue;
-      slot[t] = s.slot(pg.p[t], hk, base + 16 * t);
+      const int p = s.entry(pg, t);
+      if (base + 16 * t >= n || !s.named(p)) continue;
+      slot[t] = s.slot(p, hk, base + 16 * t);
       const uint8_t* kq = s.c.k_q + slot[t] * (D / 2) + (key * (D / 2) + 4 * kKWords * g);
       const uint8_t* ks = s.c.k_s + slot[t] * kGroups + (key * kGroups + kKWords / 2 * g);
       if constexpr (D == 128) {

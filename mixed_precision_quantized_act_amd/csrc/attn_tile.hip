@@ -42,7 +42,7 @@ __device__ __forceinline__ int k_piece(int key, int c) {
 }
 template <int D>
 __device__ __forceinline__ int v_piece(int key, int c) {
-  return key * (D * 2) + 32 * ((c >> 1) ^ (D == 128 ? key & 7 : (key >> 1) & 3)) + 16 * (c & 1);
+  return key * (D * 2) + 32 * ((c >> 1) ^ (D == 128 ? key & 7 : key & 3)) + 16 * (c & 1);
 }
 
 // Before a row has seen a key: any logit plus this gives an infinite weight,
@@ -55,64 +55,63 @@ struct Pieces {
   int n, size, whole;
 };
 
-// Staging by T threads: a thread takes units of K or of V, the same side for
-// a whole wave.
+// Staging by T threads: a thread takes kPer units, each of K or of V, the same
+// for a whole wave.  A unit is loaded a tile before it is stored; both are
+// done piece by piece in the turns of a step, beside the step's MFMAs, and
+// without branches, which would keep their scalar work from running there (all
+// at once, staging a tile took a third of the time).  So every load has a valid
+// place: past the end the last one's, whose keys nobody sees.
 template <class Source, int D, int T>
 struct Tile;
 
-__device__ __forceinline__ float row_max(const f32x16& s) {
-  float top = max3(s[0], s[1], s[2]);
-#pragma unroll
-  for (int i = 3; i < 15; i += 2) top = max3(top, s[i], s[i + 1]);
-  return pair_max(fmaxf(top, s[15]));
-}
-
-// NVFP4: a unit is a group of 16 elements.
+// NVFP4: a unit is a group of 16 elements, stored as two 16-byte pieces.
 template <int D, int T>
 struct Tile<Kv4Source, D, T> {
   static constexpr int kGroups = D / 16;
   static constexpr int kUnits = kTileKeys * kGroups;
   static constexpr int kPer = 2 * kUnits / T;
+  static constexpr int kParts = 2 * kPer;
 
-  struct Regs {
-    u32x2 w[kPer];
-    uint32_t s[kPer];              // group scale (0: not seen)
+  // a unit's fixed places (a wave's lies within one sixteen of keys)
+  struct Place {
+    const uint8_t *q, *s;          // in the slots of that sixteen
+    int key, sixteen;              // key in the tile
+    int at[2];                     // each part's place in a staged tile
   };
-  // (a wave's unit lies within one sixteen of keys: its place is uniform)
-  template <bool V>
-  static __device__ __forceinline__ void load(Regs& r, const Kv4Source& s,
-                                              const Kv4Source::Look& pg, uint64_t, int64_t, int hk,
-                                              int base, int n, int wave, int lane) {
+  struct Regs {
+    u32x2 w;
+    uint32_t s;                    // group scale
+    int left;                      // keys of the tile that have slots, from its start
+  };
+  static __device__ __forceinline__ bool is_v(int u, int wave) { return u * T + 64 * wave >= kUnits; }
+  static __device__ __forceinline__ void place(Place& r, const Kv4Source& s, int64_t, int, int u,
+                                               int wave, int lane) {
+    const bool val = is_v(u, wave);
+    const int y = (u * T + 64 * wave) & (kUnits - 1), key = (y + lane) / kGroups, g = (y + lane) % kGroups;
+    const int z = (y + lane) & (16 * kGroups - 1);         // (key % 16, group)
+    r.q = (val ? s.c.v_q : s.c.k_q) + 8 * z;
+    r.s = (val ? s.c.v_s : s.c.k_s) + z;
+    r.key = key;
+    r.sixteen = y / kGroups >> 4;
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      const int x = u * T + 64 * wave;
-      if ((x >= kUnits) != V) continue;
-      const int y = x & (kUnits - 1), t = y / kGroups >> 4;
-      const int p0 = pg.p[0], p1 = pg.p[1], p2 = pg.p[2], p3 = pg.p[3];
-      const int p = t < 2 ? (t == 0 ? p0 : p1) : (t == 2 ? p2 : p3);
-      const uint32_t z = (uint32_t)(y + lane) & (16 * kGroups - 1);       // (key % 16, group)
-      r.w[u] = u32x2{0, 0};
-      r.s[u] = 0;
-      if (s.named(p) && base + 16 * t + (int)(z / kGroups) < n) {
-        const int64_t at = s.slot(p, hk, base + 16 * t);
-        r.w[u] = *reinterpret_cast<const u32x2*>((V ? s.c.v_q : s.c.k_q) + at * (D / 2) + 8 * z);
-        r.s[u] = ((V ? s.c.v_s : s.c.k_s) + at * kGroups)[z];
-      }
-    }
+    for (int h = 0; h < 2; ++h)
+      r.at[h] = val ? v_piece<D>(key, 2 * g + h) : k_piece<D>(key, 2 * g + h);
   }
-  template <bool V>
-  static __device__ __forceinline__ void store(const Regs& r, char* to, int wave, int lane) {
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      const int x = u * T + 64 * wave;
-      if ((x >= kUnits) != V) continue;
-      const int y = (x & (kUnits - 1)) + lane, key = y / kGroups, g = y % kGroups;
-      const f16x2 sc = scale_f16<0>(r.s[u]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<u32x4*>(to + (V ? v_piece<D>(key, 2 * g + h) : k_piece<D>(key, 2 * g + h))) =
-            codes_f16(r.w[u][h], sc);
-    }
+  static __device__ __forceinline__ void load(Regs& r, const Place& pl, const Kv4Source& s,
+                                              const Kv4Source::Look& pg, uint64_t, int hk, int base,
+                                              int n) {
+    const int p = s.entry(pg, pl.sixteen), at = base + 16 * pl.sixteen;
+    const bool ok = s.named(p) && at < n;
+    const int64_t slot = s.slot(ok ? p : 0, hk, at);
+    r.w = *reinterpret_cast<const u32x2*>(pl.q + slot * (D / 2));
+    r.s = pl.s[slot * kGroups];
+    r.left = ok ? n - base : 0;
+  }
+  // part h into the staged tile `to`; what has no slot gets a scale of zero (the
+  // bytes may be a NaN's)
+  static __device__ __forceinline__ void store(const Regs& r, const Place& pl, int h, char* to) {
+    const f16x2 sc = scale_f16<0>(pl.key < r.left ? r.s : 0u);
+    *reinterpret_cast<u32x4*>(to + pl.at[h]) = codes_f16(r.w[h], sc);
   }
 };
 
@@ -122,37 +121,47 @@ struct Tile<CrossSource, D, T> {
   static constexpr int kPieces = D / 8;
   static constexpr int kUnits = kTileKeys * kPieces;
   static constexpr int kPer = 2 * kUnits / T;
+  static constexpr int kParts = kPer;
 
-  struct Regs {
-    u32x4 w[kPer];
+  struct Place {
+    const uint16_t* p;             // in state 0 of the sequence
+    int64_t ld;
+    int key, at;
   };
-  template <bool V>
-  static __device__ __forceinline__ void load(Regs& r, const CrossSource& s,
-                                              const CrossSource::Look&, uint64_t seen, int64_t b,
-                                              int hk, int base, int, int wave, int lane) {
-    const int64_t row0 = b * s.Lk + base;
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      const int x = u * T + 64 * wave;
-      if ((x >= kUnits) != V) continue;
-      const int y = (x & (kUnits - 1)) + lane, key = y / kPieces, c = y % kPieces;
-      r.w[u] = u32x4{0, 0, 0, 0};
-      if ((seen >> key) & 1)             // (what is not seen may hold NaN: zeros)
-        r.w[u] = *reinterpret_cast<const u32x4*>(
-            (V ? s.v + (row0 + key) * s.ldv : s.k + (row0 + key) * s.ldk) + hk * D + 8 * c);
-    }
+  struct Regs {
+    u32x4 w;
+    uint64_t seen;
+  };
+  static __device__ __forceinline__ bool is_v(int u, int wave) { return u * T + 64 * wave >= kUnits; }
+  static __device__ __forceinline__ void place(Place& r, const CrossSource& s, int64_t b, int hk,
+                                               int u, int wave, int lane) {
+    const bool val = is_v(u, wave);
+    const int y = ((u * T + 64 * wave) & (kUnits - 1)) + lane, key = y / kPieces, c = y % kPieces;
+    r.ld = val ? s.ldv : s.ldk;
+    r.p = (val ? s.v : s.k) + b * s.Lk * r.ld + hk * D + 8 * c;
+    r.key = key;
+    r.at = val ? v_piece<D>(key, c) : k_piece<D>(key, c);
   }
-  template <bool V>
-  static __device__ __forceinline__ void store(const Regs& r, char* to, int wave, int lane) {
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      const int x = u * T + 64 * wave;
-      if ((x >= kUnits) != V) continue;
-      const int y = (x & (kUnits - 1)) + lane, key = y / kPieces, c = y % kPieces;
-      *reinterpret_cast<u32x4*>(to + (V ? v_piece<D>(key, c) : k_piece<D>(key, c))) = r.w[u];
-    }
+  static __device__ __forceinline__ void load(Regs& r, const Place& pl, const CrossSource&,
+                                              const CrossSource::Look&, uint64_t seen, int,
+                                              int base, int n) {
+    r.w = *reinterpret_cast<const u32x4*>(pl.p + min(base + pl.key, n - 1) * pl.ld);
+    r.seen = seen;
+  }
+  // (what is not seen may hold NaN: zeros)
+  static __device__ __forceinline__ void store(const Regs& r, const Place& pl, int, char* to) {
+    const bool on = (r.seen >> pl.key) & 1;
+    *reinterpret_cast<u32x4*>(to + pl.at) = u32x4{on ? r.w[0] : 0u, on ? r.w[1] : 0u,
+                                                  on ? r.w[2] : 0u, on ? r.w[3] : 0u};
   }
 };
+
+__device__ __forceinline__ float row_max(const f32x16& s) {
+  float top = max3(s[0], s[1], s[2]);
+#pragma unroll
+  for (int i = 3; i < 15; i += 2) top = max3(top, s[i], s[i + 1]);
+  return pair_max(fmaxf(top, s[15]));
+}
 
 // One wave's rows: 32, a lane's row is its column of S^T (both halves of the
 // wave hold it, each half its keys).
@@ -203,22 +212,27 @@ struct Rows {
   }
 
   // Step: settle the weights p (formed from `next`, their sum in `sum`); then
-  // the logits of 32 keys (K at k + ka, into `next`) and the second product of
-  // p (V at v + va) alternate with the weights of s, which go to pn and `sum`.
-  template <int KO, int VO>
+  // the logits of 32 keys (K at ka + KV, into `next`) and the second product of
+  // p (V at va + KV) alternate with the weights of s, which go to pn and `sum`.
+  // `head`: the first operands, read in the step before; this step reads those
+  // of the next one (ka, va moved on by ks, vs, at offset NEXT).  side(i): what
+  // else is done in turn i of 8.
+  static constexpr int kN = 2 * (D / 16);       // products, of the two kinds in turn
+  static constexpr int kAhead = 4;              // operands read ahead
+  template <int KV>
+  __device__ __forceinline__ u32x4 operand(int g, const char* k, const int (&ka)[D / 16],
+                                           const char* v, const int (&va)[D / 32]) {
+    return g & 1 ? v_operand<KV>(v, va, g / 2 / (D / 32), g / 2 % (D / 32))
+                 : *reinterpret_cast<const u32x4*>(k + KV + ka[g / 2]);
+  }
+  template <int KV, int NEXT, class Side>
   __device__ __forceinline__ void step(const f32x16& s, u32x4 (&pn)[2], f32x16& next,
-                                       u32x4 (&p)[2], float& sum, const char* k,
-                                       const int (&ka)[D / 16], const char* v,
-                                       const int (&va)[D / 32]) {
-    constexpr int kN = 2 * (D / 16);            // products, of the two kinds in turn
-    constexpr int kAhead = 4;                   // operands read ahead
-    u32x4 f[kN];
-    auto fetch = [&](int g) {
-      f[g] = g & 1 ? v_operand<VO>(v, va, g / 2 / (D / 32), g / 2 % (D / 32))
-                   : *reinterpret_cast<const u32x4*>(k + KO + ka[g / 2]);
-    };
+                                       u32x4 (&p)[2], float& sum, u32x4 (&head)[kAhead],
+                                       const char* k, int (&ka)[D / 16], const char* v,
+                                       int (&va)[D / 32], int ks, int vs, Side side) {
+    u32x4 f[kN + kAhead];
 #pragma unroll
-    for (int g = 0; g < kAhead; ++g) fetch(g);
+    for (int g = 0; g < kAhead; ++g) f[g] = head[g];
     settle(next, p, sum);
     next = f32x16{};
     // the weights of pair i in stages, one a turn, so that no instruction waits
@@ -229,9 +243,20 @@ struct Rows {
     x[1] = __builtin_fmaf(s[1], c, shift);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      side(i);
 #pragma unroll
       for (int g = i * kN / 8; g < (i + 1) * kN / 8; ++g) {
-        if (g + kAhead < kN) fetch(g + kAhead);
+        if (g + kAhead < kN) {
+          f[g + kAhead] = operand<KV>(g + kAhead, k, ka, v, va);
+        } else {
+          if (g + kAhead == kN) {
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) ka[d] += ks;
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) va[d] += vs;
+          }
+          f[g + kAhead] = operand<NEXT>(g + kAhead - kN, k, ka, v, va);
+        }
         if (g & 1)
           o[g / 2 % (D / 32)] = mfma32<F16>(f[g], p[g / 2 / (D / 32)], o[g / 2 % (D / 32)]);
         else
@@ -249,6 +274,8 @@ struct Rows {
     }
     pn[1][3] = pack16<F16>(x[14], x[15]);
     sum = mfma16<F16>(ones, pn[1], total)[0];
+#pragma unroll
+    for (int g = 0; g < kAhead; ++g) head[g] = f[kN + g];
   }
   // V^T of 16 keys s16 and elements 32 d .. as the second product's operand
   template <int VO>
@@ -297,10 +324,11 @@ __device__ __forceinline__ void hide(f32x16& s, uint32_t seen, int left, int h) 
 // running fastest.  W waves of 32 rows each.
 //
 // Tile t is computed in two steps of 32 keys, each with the logits of the
-// step after it and the second product of the step before it, so K is needed
-// one step before V of the same keys and V one step after: K of tile t + 1 is
-// written to shared memory in the first step of tile t, before the only
-// barrier, V in the second.
+// step after it and the second product of the step before it.  Shared memory
+// holds three tiles of K and of V: between the middles of the second steps of
+// tiles t - 1 and t, where the workgroup meets, K(t), V(t - 1), K(t + 1) and
+// V(t) are read and K(t + 2) and V(t + 1) written, which replace K(t - 1) and
+// V(t - 2), read before.  So operands can be read ahead across the steps.
 template <class Source, int D, int W>
 __global__ void __launch_bounds__(64 * W, 2)
 attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, Pieces pc, Gate gate) {
@@ -308,8 +336,8 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, Pieces pc, Gat
   using T = Tile<Source, D, 64 * W>;
   constexpr bool kF16 = Source::kF16;
   constexpr int kBytes = kTileKeys * D * 2, kHalf = kBytes / 2;
-  __shared__ __align__(16) char kt[2 * kBytes];            // two tiles
-  __shared__ __align__(16) char vt[2 * kBytes];
+  __shared__ __align__(16) char kt[3 * kBytes];            // three tiles
+  __shared__ __align__(16) char vt[3 * kBytes];
 
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -337,15 +365,31 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, Pieces pc, Gat
   // tiles of which this wave's rows see anything
   const int mine = min(nt, max(0, (wend - base0 + kTileKeys - 1) / kTileKeys));
 
-  typename T::Regs regs = {};
-  typename Source::Look look = {};
-  uint64_t seen = 0, seen_next = 0;
+  // seen[j]: the keys of tile t + j; look_v, look_k: what the loads of V(t + 2)
+  // and K(t + 3) need.
+  typename T::Place place[T::kPer];
+  typename T::Regs regs[T::kPer], first[T::kPer], second[T::kPer];
+  typename Source::Look look_v = {}, look_k = {};
+  uint64_t seen[4] = {0, 0, 0, 0};
   if (nt > 0) {
-    look = src.look(b, base0, n, lane);
-    seen = src.seen(look, base0, n, lane);
-    T::template load<false>(regs, src, look, seen, b, hk, base0, n, wave, lane);
-    T::template load<true>(regs, src, look, seen, b, hk, base0, n, wave, lane);
-    look = src.look(b, base0 + kTileKeys, n, lane);
+    const typename Source::Look look0 = src.look(b, base0, n, lane);
+    const typename Source::Look look1 = src.look(b, base0 + kTileKeys, n, lane);
+    look_v = src.look(b, base0 + 2 * kTileKeys, n, lane);
+    look_k = src.look(b, base0 + 3 * kTileKeys, n, lane);
+    seen[0] = src.seen(look0, base0, n, lane);
+    seen[1] = src.seen(look1, base0 + kTileKeys, n, lane);
+    seen[2] = src.seen(look_v, base0 + 2 * kTileKeys, n, lane);
+#pragma unroll
+    for (int u = 0; u < T::kPer; ++u) {
+      const int base1 = base0 + kTileKeys, base2 = base1 + kTileKeys;
+      T::place(place[u], src, b, hk, u, wave, lane);
+      T::load(first[u], place[u], src, look0, seen[0], hk, base0, n);
+      T::load(second[u], place[u], src, look1, seen[1], hk, base1, n);
+      if (T::is_v(u, wave))
+        regs[u] = second[u];
+      else
+        T::load(regs[u], place[u], src, look_v, seen[2], hk, base2, n);
+    }
   }
 
   const int row = row0 + col, t = row / G;
@@ -382,52 +426,81 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, Pieces pc, Gat
   f32x16 s0 = {}, s1 = {};
   u32x4 p0[2] = {}, p1[2] = {};
   float sum = 0.0f;
+  u32x4 ahead[Rows<kF16, D>::kAhead];
   if (nt > 0) {
-    T::template store<false>(regs, kt, wave, lane);
-    T::template store<true>(regs, vt, wave, lane);
+#pragma unroll
+    for (int j = 0; j < T::kParts; ++j) {
+      const int u = j * T::kPer / T::kParts, part = j % (T::kParts / T::kPer);
+      T::store(first[u], place[u], part, T::is_v(u, wave) ? vt : kt);
+      if (!T::is_v(u, wave)) T::store(second[u], place[u], part, kt + kBytes);
+    }
     __syncthreads();
-    if (mine > 0) r.logits(s0, kt, ka);
+    if (mine > 0) {
+      r.logits(s0, kt, ka);
+#pragma unroll
+      for (int g = 0; g < Rows<kF16, D>::kAhead; ++g)
+        ahead[g] = r.template operand<kHalf>(g, kt, ka, vt, va);
+    }
   }
-  // the next tile's loads; V's are stored in the second step
-  auto fetch = [&](int base) {
-    seen_next = src.seen(look, base, n, lane);
-    T::template load<false>(regs, src, look, seen_next, b, hk, base, n, wave, lane);
-    T::template load<true>(regs, src, look, seen_next, b, hk, base, n, wave, lane);
-    look = src.look(b, base + kTileKeys, n, lane);
+  // The tile's turns of staging.  slot: i % 3; the tiles that are stored come
+  // after the last one, too (into places that nobody reads any more).
+  int slot = 0;
+  auto store_turn = [&](int turn) {
+#pragma unroll
+    for (int j = 0; j < T::kParts; ++j)
+      if (turn == 1 + j * 6 / T::kParts) {
+        const int u = j * T::kPer / T::kParts, part = j % (T::kParts / T::kPer);
+        const int k = (slot == 0 ? 2 : slot - 1) * kBytes, v = (slot == 2 ? 0 : slot + 1) * kBytes;
+        T::store(regs[u], place[u], part, T::is_v(u, wave) ? vt + v : kt + k);
+      }
+  };
+  auto load_turn = [&](int turn, int base) {         // base: of tile i
+#pragma unroll
+    for (int u = 0; u < T::kPer; ++u)
+      if (turn == 1 + u * 3 / T::kPer) {
+        const bool val = T::is_v(u, wave);
+        typename Source::Look look = look_k;
+        if (val) look = look_v;
+        T::load(regs[u], place[u], src, look, val ? seen[2] : seen[3], hk,
+                base + (val ? 2 : 3) * kTileKeys, n);
+      }
+    if (turn == 0) seen[3] = src.seen(look_k, base + 3 * kTileKeys, n, lane);
+    if (turn == 5) {
+      look_v = look_k;
+      look_k = src.look(b, base + 4 * kTileKeys, n, lane);
+      seen[0] = seen[1];
+      seen[1] = seen[2];
+      seen[2] = seen[3];
+      slot = slot == 2 ? 0 : slot + 1;
+    }
   };
   int i = 0;
   for (; i < mine; ++i) {
-    const int base = base0 + i * kTileKeys, other = i & 1 ? 0 : kBytes;
-    const bool more = i + 1 < nt;
-    if (more) fetch(base + kTileKeys);
-    const bool whole = seen == ~0ull && base + kTileKeys <= all;
+    const int base = base0 + i * kTileKeys;
+    const uint64_t here = seen[0];
+    const bool whole = here == ~0ull && base + kTileKeys <= all;
     // `va` is at the tile before (in the first there is none: weights of zero
-    // on this tile's values), `ka` at this one
-    if (!whole) hide(s0, (uint32_t)seen, upto - base, h);
-    r.template step<kHalf, kHalf>(s0, p0, s1, p1, sum, kt, ka, vt, va);
-    if (more) T::template store<false>(regs, kt + other, wave, lane);
-    __syncthreads();
-    // on to the next tile of K (after the last: logits that nobody looks at)
-    // and to this one of V
-    const int ks = more ? (i & 1 ? -kBytes : kBytes) : 0, vs = i == 0 ? 0 : (i & 1 ? kBytes : -kBytes);
-#pragma unroll
-    for (int d = 0; d < D / 16; ++d) ka[d] += ks;
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d) va[d] += vs;
-    if (!whole) hide(s1, (uint32_t)(seen >> 32), upto - base - 32, h);
-    r.template step<0, 0>(s1, p1, s0, p0, sum, kt, ka, vt, va);
-    if (more) T::template store<true>(regs, vt + other, wave, lane);
-    seen = seen_next;
+    // on this tile's values), `ka` at this one; on to the next tile of K (after
+    // the last: logits that nobody looks at) and to this one of V
+    const int ks = slot == 2 ? -2 * kBytes : kBytes;
+    const int vs = i == 0 ? 0 : slot == 0 ? -2 * kBytes : kBytes;
+    if (!whole) hide(s0, (uint32_t)here, upto - base, h);
+    r.template step<kHalf, 0>(s0, p0, s1, p1, sum, ahead, kt, ka, vt, va, ks, vs,
+                              [&](int turn) { store_turn(turn); });
+    if (!whole) hide(s1, (uint32_t)(here >> 32), upto - base - 32, h);
+    r.template step<0, kHalf>(s1, p1, s0, p0, sum, ahead, kt, ka, vt, va, 0, 0, [&](int turn) {
+      load_turn(turn, base);
+      if (turn == 4) __syncthreads();
+    });
   }
   if (mine > 0) r.template second<kHalf>(s1, p1, sum, vt, va);
   // tiles that only other waves' rows see
   for (; i < nt; ++i) {
-    const int base = base0 + i * kTileKeys, other = i & 1 ? 0 : kBytes;
-    const bool more = i + 1 < nt;
-    if (more) fetch(base + kTileKeys);
-    if (more) T::template store<false>(regs, kt + other, wave, lane);
+#pragma unroll
+    for (int turn = 0; turn < 8; ++turn) store_turn(turn);
+#pragma unroll
+    for (int turn = 0; turn < 8; ++turn) load_turn(turn, base0 + i * kTileKeys);
     __syncthreads();
-    if (more) T::template store<true>(regs, vt + other, wave, lane);
   }
 
   const float lt = r.l;
@@ -465,24 +538,22 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, Pieces pc, Gat
 }
 
 // rows of a workgroup
-constexpr int kTileRows = 256;
+constexpr int kTileWaves = 8;
+constexpr int kTileRows = 32 * kTileWaves;
 
-// Two workgroups fit a CU: this many run at once.  Row tiles that do not fill
+// One workgroup fits a CU: this many run at once.  Row tiles that do not fill
 // them (or fill them badly) have their keys cut into pieces: S equal ones, or
 // as many large ones as fit at once and a small one for the places that are
-// left, which takes each of those several times.  The cost in units of a
-// tile's keys: the time of the slowest place, a workgroup alone on its CU
-// at 3/4 of the time; and for more than one piece the partial sums, written
-// and read again, and the launch that joins them.
-//   1350 rows x 30 heads of 64, 12376 keys (180 row tiles): 1 piece 305 us, 2
-//   254 us, 4 210 us (3 large and small: see the header).
+// left, which takes each of those several times.  The cost in us: the
+// time of the slowest place, and for more than one piece the partial sums,
+// written and read again, and the launch that joins them.
 constexpr int64_t kPlaces = 256;
 
 Pieces pieces_of(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L, size_t ws_bytes) {
   const int64_t rows = B * Lq * Hq;
   const int64_t u = B * Hkv * ((Lq * (Hq / Hkv) + kTileRows - 1) / kTileRows);
   const int64_t chunks = (L + kTileKeys - 1) / kTileKeys;
-  const double tau = D == 64 ? 2.0 : 4.0;                      // us a tile of keys
+  const double tau = D == 64 ? 1.1 : 1.9;                      // us a tile of keys
   const int64_t fit = (int64_t)(ws_bytes / AttnSplit::bytes(rows, D));
   Pieces best = {1, 1, 1};
   double least = 0.0;
@@ -493,8 +564,7 @@ Pieces pieces_of(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L, size_
       double span;                                              // of the slowest place, of `whole`
       if (!uneven) {
         const int64_t k = u * n;
-        const int64_t rest = k % kPlaces;
-        span = (double)(k / kPlaces) + (rest == 0 ? 0.0 : rest <= kPlaces / 2 ? 0.75 : 1.0);
+        span = (double)((k + kPlaces - 1) / kPlaces);
       } else {
         const int64_t left = kPlaces - u * (n - 1);             // places beside the large pieces
         if (n < 2 || left <= 0) continue;
@@ -534,10 +604,10 @@ hipError_t launch_attn_tile(const AttnArgs& a, const Source& src, int64_t L, voi
   const int64_t tiles = (a.Lq * (a.Hq / a.Hkv) + kTileRows - 1) / kTileRows;
   const dim3 grid((unsigned)(a.B * a.Hkv * pc.n * tiles));
   if (a.D == 64)
-    hipLaunchKernelGGL((attn_tile_kernel<Source, 64, 8>), grid, dim3(512), 0, stream, a, src,
+    hipLaunchKernelGGL((attn_tile_kernel<Source, 64, kTileWaves>), grid, dim3(64 * kTileWaves), 0, stream, a, src,
                        sp, (int)tiles, pc, gt);
   else
-    hipLaunchKernelGGL((attn_tile_kernel<Source, 128, 8>), grid, dim3(512), 0, stream, a, src,
+    hipLaunchKernelGGL((attn_tile_kernel<Source, 128, kTileWaves>), grid, dim3(64 * kTileWaves), 0, stream, a, src,
                        sp, (int)tiles, pc, gt);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || pc.n == 1) return e;
