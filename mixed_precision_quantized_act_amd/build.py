@@ -19,7 +19,7 @@ OBJ_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["act_quant.hip", "qgemm.hip", "qgemm_i8.hip", "tdc.hip", "noalloc.hip", "convert_check.hip", "stage_ab.hip",
            "qgemv.hip", "qk_norm.hip", "kv4.hip", "attn.hip", "attn_few.hip",
-           "attn_tile.hip", "abi.cpp"]
+           "attn_tile.hip", "attn_short.hip", "abi.cpp"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

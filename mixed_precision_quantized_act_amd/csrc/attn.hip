@@ -39,7 +39,9 @@ hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4Cache& c, const int32_t* 
 hipError_t launch_attn_cross(const AttnArgs& a, const uint16_t* k, int64_t ldk, const uint16_t* v,
                              int64_t ldv, int64_t Lk, const int32_t* k_lens, const uint8_t* mask,
                              void* ws, size_t ws_bytes, hipStream_t stream) {
-  return launch(a, CrossSource{k, v, ldk, ldv, (int)Lk, k_lens, mask}, Lk, ws, ws_bytes, stream);
+  const CrossSource src = {k, v, ldk, ldv, (int)Lk, k_lens, mask};
+  if (attn_short_takes(a.B, a.Lq, a.Hq, a.Hkv, Lk)) return launch_attn_short(a, src, stream);
+  return launch(a, src, Lk, ws, ws_bytes, stream);
 }
 
 }  // namespace qact
