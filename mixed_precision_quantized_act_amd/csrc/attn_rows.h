@@ -226,6 +226,18 @@ __device__ __forceinline__ void hide(f32x16& s, uint32_t seen, int left, int h) 
     s[i] = bits & (1u << (8 * (i >> 2) + (i & 3))) ? s[i] : -INFINITY;
 }
 
+// The same where all rows see the same keys (the bits become lane masks on the
+// scalar unit: one VALU instruction an element, not three).
+__device__ __forceinline__ void hide(f32x16& s, uint32_t seen) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int key = 8 * (i >> 2) + (i & 3);
+    const uint64_t lo = (uint32_t)((int32_t)(seen << (31 - key)) >> 31);
+    const uint64_t hi = (uint32_t)((int32_t)(seen << (27 - key)) >> 31);
+    s[i] = __builtin_amdgcn_inverse_ballot_w64(hi << 32 | lo) ? s[i] : -INFINITY;
+  }
+}
+
 // A wave's finished rows, rounded to bf16, to `dst` (the lane's row and head).
 template <bool F16, int D>
 __device__ __forceinline__ void store_rows(const Rows<F16, D>& r, float v_scale, uint16_t* dst, int h,

@@ -4,8 +4,12 @@
 // rows, 32 at a time, without meeting again; the next 32 are on their way
 // meanwhile.  attn_rows.h says what a wave does with them.
 //
-// One pass of 32 rows over 256 states (heads of 64) takes 2.9 us of a SIMD
-// that two waves share, against 0.9 us that its bytes take of the memory.
+// 30 heads of 64, 17550 query tokens, 226 states: 61 us, 0.50 us of a SIMD for
+// 32 rows by 64 keys (the alternating products and weights alone take 0.41 us
+// of it) and 27 us for the rest: launch, staging, each block's first and last
+// products and its rows' load and store.  A memory that is read and written
+// once would take 27 us.  Stored as whole lines through shared memory, the rows
+// cost 1 us less; 12 waves instead of 8 spill registers and cost 6 us more.
 #include "attn_rows.h"
 
 namespace qact {
@@ -21,6 +25,7 @@ template <int D>
 __global__ void __launch_bounds__(64 * kShortWaves, 2)
 attn_short_kernel(AttnArgs a, CrossSource src, int blocks, int shares, Gate gate) {
   if (gated_off(gate)) return;
+  constexpr int W = kShortWaves;
   using R = Rows<false, D>;
   constexpr int kBytes = kTileKeys * D * 2, kHalf = kBytes / 2, kPieces = D / 8;
   // K, V, and half a tile of zeros: the values before the first tile
@@ -42,33 +47,36 @@ attn_short_kernel(AttnArgs a, CrossSource src, int blocks, int shares, Gate gate
 
   u32x4 next[D / 16];
   auto fetch = [&](int block) {
-    const int row = min(32 * block + col, rows - 1), t = row / G;
+    const int row = min(32 * block + col, rows - 1), t = G == 1 ? row : row / G;
     const uint16_t* p = a.q + (b * a.Lq + t) * a.ldq + (int64_t)(hk * G + row - t * G) * D + 8 * h;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) next[i] = *reinterpret_cast<const u32x4*>(p + 16 * i);
   };
   if (block < last) fetch(block);
+  // a thread's pieces of the keys; what is not seen may hold NaN and is zeroed
+  // when that is known
+  constexpr int kLoads = kShortTiles * kTileKeys * kPieces / (64 * W);
+  u32x4 kr[kLoads], vr[kLoads];
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) {
+    const int x = u * 64 * W + tid, c = x % kPieces;
+    const int64_t row = b * src.Lk + min((int64_t)(x / kPieces), src.Lk - 1);
+    kr[u] = *reinterpret_cast<const u32x4*>(src.k + row * src.ldk + hk * D + 8 * c);
+    vr[u] = *reinterpret_cast<const u32x4*>(src.v + row * src.ldv + hk * D + 8 * c);
+  }
 
   uint64_t seen[kShortTiles];
 #pragma unroll
   for (int t = 0; t < kShortTiles; ++t)
     seen[t] = src.seen(src.look(b, t * kTileKeys, n, lane), t * kTileKeys, n, lane);
-  // a thread's piece of every eighth (heads of 64) or sixteenth of the keys
 #pragma unroll
-  for (int t = 0; t < kShortTiles; ++t)
-    if (t < nt)
-#pragma unroll
-      for (int u = 0; u < kTileKeys * kPieces / (64 * kShortWaves); ++u) {
-        const int x = u * 64 * kShortWaves + tid, key = x / kPieces, c = x % kPieces;
-        u32x4 k = {0, 0, 0, 0}, v = {0, 0, 0, 0};
-        if ((seen[t] >> key) & 1) {      // (what is not seen may hold NaN: zeros)
-          const int64_t row = b * src.Lk + t * kTileKeys + key;
-          k = *reinterpret_cast<const u32x4*>(src.k + row * src.ldk + hk * D + 8 * c);
-          v = *reinterpret_cast<const u32x4*>(src.v + row * src.ldv + hk * D + 8 * c);
-        }
-        *reinterpret_cast<u32x4*>(kt + t * kBytes + k_piece<D>(key, c)) = k;
-        *reinterpret_cast<u32x4*>(vt + t * kBytes + v_piece<D>(key, c)) = v;
-      }
+  for (int u = 0; u < kLoads; ++u) {
+    constexpr int kOf = kTileKeys * kPieces / (64 * W);         // loads of a tile
+    const int t = u / kOf, x = u % kOf * 64 * W + tid, key = x / kPieces, c = x % kPieces;
+    if (!((seen[t] >> key) & 1)) kr[u] = vr[u] = u32x4{0, 0, 0, 0};
+    *reinterpret_cast<u32x4*>(kt + t * kBytes + k_piece<D>(key, c)) = kr[u];
+    *reinterpret_cast<u32x4*>(vt + t * kBytes + v_piece<D>(key, c)) = vr[u];
+  }
   if (tid < kHalf / 16) *reinterpret_cast<u32x4*>(vt + kZeros + kHalf + 16 * tid) = u32x4{0, 0, 0, 0};
   __syncthreads();
 
@@ -81,10 +89,10 @@ attn_short_kernel(AttnArgs a, CrossSource src, int blocks, int shares, Gate gate
   R r;
   r.set_ones(lane);
   r.c = fmaxf(a.scale * kLog2e, 0x1p-126f);
-  for (; block < last; block += kShortWaves) {
+  for (; block < last; block += W) {
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) r.q[i] = next[i];
-    if (block + kShortWaves < last) fetch(block + kShortWaves);
+    fetch(min(block + W, last - 1));
     r.clear();
     if (nt > 0) {
       f32x16 s0, s1 = {};
@@ -96,11 +104,11 @@ attn_short_kernel(AttnArgs a, CrossSource src, int blocks, int shares, Gate gate
 #pragma unroll 1
       for (int t = 0; t < nt; ++t) {
         const uint64_t here = t < 2 ? (t == 0 ? seen[0] : seen[1]) : (t == 2 ? seen[2] : seen[3]);
-        if ((uint32_t)here != ~0u) hide(s0, (uint32_t)here, 32, h);
+        if ((uint32_t)here != ~0u) hide(s0, (uint32_t)here);
         if (t == 0) r.start(s0);
         r.template step<kHalf, 0>(s0, p0, s1, p1, sum, ahead, kt, ka, vt, va, kBytes,
                                   t == 0 ? -kZeros : kBytes, [](int) {});
-        if ((uint32_t)(here >> 32) != ~0u) hide(s1, (uint32_t)(here >> 32), 32, h);
+        if ((uint32_t)(here >> 32) != ~0u) hide(s1, (uint32_t)(here >> 32));
         r.template step<0, kHalf>(s1, p1, s0, p0, sum, ahead, kt, ka, vt, va, 0, 0, [](int) {});
       }
       r.template second<kHalf>(s1, p1, sum, vt, va);
@@ -109,7 +117,10 @@ attn_short_kernel(AttnArgs a, CrossSource src, int blocks, int shares, Gate gate
 #pragma unroll
       for (int d = 0; d < D / 32; ++d) va[d] += kZeros - (nt - 1) * kBytes;
     }
-    const int row = 32 * block + col, t = row / G;
+    // wait for the next rows here, not behind the stores of these
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) asm volatile("" : "+v"(next[i]));
+    const int row = 32 * block + col, t = G == 1 ? row : row / G;
     store_rows(r, 1.0f, a.o + (b * a.Lq + t) * a.ldo + (int64_t)(hk * G + row - t * G) * D, h,
                row < rows);
   }
@@ -118,37 +129,38 @@ attn_short_kernel(AttnArgs a, CrossSource src, int blocks, int shares, Gate gate
 // Workgroups that run at once, and the time (us) of staging and of one pass of
 // the waves of each.
 constexpr int64_t kPlaces = 256;
-constexpr double kStage = 3.0, kPass64 = 3.2;
+constexpr double kStage = 3.0, kPass = 3.2;
 
 }  // namespace
 
 bool attn_short_takes(int64_t B, int64_t Lq, int Hq, int Hkv, int64_t Lk) {
-  return Lk <= kShortTiles * kTileKeys && Lq * (Hq / Hkv) >= 32 * kShortWaves;
+  return Lk >= 1 && Lk <= kShortTiles * kTileKeys && Lq * (Hq / Hkv) >= 256;
 }
 
-hipError_t launch_attn_short(const AttnArgs& a, const CrossSource& src, hipStream_t stream) {
+template <int D>
+static hipError_t launch(const AttnArgs& a, const CrossSource& src, hipStream_t stream) {
+  constexpr int W = kShortWaves;
   const int64_t units = a.B * a.Hkv;
   const int blocks = (int)((a.Lq * (a.Hq / a.Hkv) + 31) / 32);
   // shares of a head's rows: the rounds of workgroups times the passes of each
   int shares = 1;
   double least = 0.0;
-  for (int s = 1; s <= 64 && (s == 1 || s * kShortWaves <= blocks); ++s) {
+  for (int s = 1; s <= 64 && (s == 1 || s * W <= blocks); ++s) {
     const int64_t rounds = (units * s + kPlaces - 1) / kPlaces;
-    const int64_t passes = (blocks + (int64_t)s * kShortWaves - 1) / ((int64_t)s * kShortWaves);
-    const double cost = (double)rounds * (kStage + (double)passes * kPass64);
+    const int64_t passes = (blocks + (int64_t)s * W - 1) / ((int64_t)s * W);
+    const double cost = (double)rounds * (kStage + (double)passes * kPass);
     if (s == 1 || cost < least) {
       least = cost;
       shares = s;
     }
   }
-  const dim3 grid((unsigned)(units * shares)), block(64 * kShortWaves);
-  if (a.D == 64)
-    hipLaunchKernelGGL((attn_short_kernel<64>), grid, block, 0, stream, a, src, blocks, shares,
-                       current_gate());
-  else
-    hipLaunchKernelGGL((attn_short_kernel<128>), grid, block, 0, stream, a, src, blocks, shares,
-                       current_gate());
+  hipLaunchKernelGGL((attn_short_kernel<D>), dim3((unsigned)(units * shares)), dim3(64 * W), 0,
+                     stream, a, src, blocks, shares, current_gate());
   return hipGetLastError();
+}
+
+hipError_t launch_attn_short(const AttnArgs& a, const CrossSource& src, hipStream_t stream) {
+  return a.D == 64 ? launch<64>(a, src, stream) : launch<128>(a, src, stream);
 }
 
 }  // namespace qact
