@@ -141,7 +141,8 @@ def _stream(stream):
     if stream is not None:
         return stream
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    # (the handle alone: building a torch.cuda.Stream takes 3 us a call)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _nbytes(t):
@@ -387,11 +388,11 @@ def _on(dtype, *tensors):
     for t in tensors:
         if t is None:
             continue
-        if t.dtype != dtype and not (dtype == torch.bfloat16 and t.dtype == torch.int16):
+        if t.dtype is not dtype and not (dtype is torch.bfloat16 and t.dtype is torch.int16):
             raise ValueError(f"expected a {dtype} tensor, got {t.dtype}")
         if t.get_device() != dev:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
-        if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
+        if not t.is_contiguous() and t.stride(-1) != 1 and t.shape[-1] > 1:
             raise ValueError("a tensor's last dimension must be contiguous")
 
 
@@ -403,9 +404,10 @@ def _whole(*tensors):
 
 def _rows(t, rows, width, name):
     """Row stride of a 2-D tensor of at least rows x width elements."""
-    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < width:
-        raise ValueError(f"{name}: needs shape [{rows}, {width}], got {tuple(t.shape)}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (t.shape[1] + 7) // 8 * 8)
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < rows or shape[1] < width:
+        raise ValueError(f"{name}: needs shape [{rows}, {width}], got {tuple(shape)}")
+    return t.stride(0) if shape[0] > 1 else max(t.stride(0), (shape[1] + 7) // 8 * 8)
 
 
 def _sized(t, n, name):
