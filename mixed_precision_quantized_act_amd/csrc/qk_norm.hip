@@ -11,8 +11,14 @@
 // Everything is float32 between one read and one rounding to bf16, so the
 // bound is the memory rate: 4 bytes per element and the position's cosines
 // and sines.  A head is spread over D/8 lanes (16 bytes each, padded to a
-// power of two for the sums); a wave takes several heads of ONE token, so
-// that the token's table row is read once per wave and not once per head.
+// power of two for the sums); a wave takes several query or several key heads
+// of ONE token, so that the token's table row and the norm's weights are read
+// once per wave and not once per head.
+//
+// 17776 tokens, 30 + 30 heads of 64, layer norm, pairs: 60 us, 273 MB at 4.5
+// TB/s (a copy reaches 5.1).  What is left to do per element is the VALU's
+// work; exchanges through shared memory, weights of both kinds per wave, and
+// a division of 64 bits took it from 60 to 78 us.
 #include "qact_device.h"
 #include "qact_internal.h"
 
@@ -20,7 +26,7 @@ namespace qact {
 
 namespace {
 
-// heads of a token taken one after the other by a lane group
+// heads of a token taken one after the other by a lane group (2: 65 us, 8: 75)
 constexpr int kQkHeads = 4;
 
 __device__ __forceinline__ void unpack8(u32x4 w, float (&f)[8]) {
@@ -31,37 +37,56 @@ __device__ __forceinline__ void unpack8(u32x4 w, float (&f)[8]) {
   }
 }
 
-// Sum over the LPH lanes of a head.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL,
+                                                               0xF, 0xF, false));
+}
+
+// Sum over the LPH lanes of a head, by lane moves that need no shared memory:
+// neighbours, pairs, then mirrors of 8 and 16 lanes (their halves hold equal
+// sums).
 template <int LPH>
 __device__ __forceinline__ float head_sum(float v) {
-#pragma unroll
-  for (int o = LPH / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, LPH);
+  v += dpp<0xB1>(v);                                             // quad_perm 1 0 3 2
+  if constexpr (LPH >= 4) v += dpp<0x4E>(v);                     // quad_perm 2 3 0 1
+  if constexpr (LPH >= 8) v += dpp<0x141>(v);                    // row_half_mirror
+  if constexpr (LPH >= 16) v += dpp<0x140>(v);                   // row_mirror
+  if constexpr (LPH >= 32) v += __shfl_xor(v, 16, 64);
   return v;
+}
+
+// 1 / sqrt(v) to one last place of float32; the hardware's takes a subnormal
+// number for zero.
+__device__ __forceinline__ float inverse_sqrt(float v) {
+  const bool small = v < 0x1p-100f;
+  return __builtin_amdgcn_rsqf(small ? v * 0x1p100f : v) * (small ? 0x1p50f : 1.0f);
 }
 
 template <int LPH, int U>
 __global__ void __launch_bounds__(256)
-qk_norm_rope_kernel(QkArgs a, int chunks, Gate gate) {
+qk_norm_rope_kernel(QkArgs a, int qchunks, int chunks, Gate gate) {
   if (gated_off(gate)) return;
   const int lane = threadIdx.x & 63;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (item >= a.M * chunks) return;
-  const int64_t tok = item / chunks;
-  const int l = lane & (LPH - 1);
-  const int head0 = (int)(item - tok * chunks) * (64 / LPH * U) + lane / LPH;
-  const int D = a.D, H = a.Hq + a.Hk;
+  const uint32_t item = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (item >= (uint32_t)(a.M * chunks)) return;           // (below 2^26)
+  const int64_t tok = item / (uint32_t)chunks;
+  const int l = lane & (LPH - 1), chunk = (int)(item % (uint32_t)chunks);
+  const int D = a.D;
   const bool in = 8 * l < D;
+  // the wave's heads: query heads or key heads
+  const bool key = chunk >= qchunks;
+  const int H = key ? a.Hk : a.Hq;
+  const int head0 = (key ? chunk - qchunks : chunk) * (64 / LPH * U) + lane / LPH;
+  const uint16_t* const src = key ? a.k + tok * a.ldk : a.q + tok * a.ldq;
+  uint16_t* const dst = key ? a.k_out + tok * a.ldko : a.q_out + tok * a.ldqo;
 
   u32x4 raw[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int h = head0 + u * (64 / LPH);
     raw[u] = u32x4{0, 0, 0, 0};
-    if (in && h < H) {
-      const uint16_t* p = h < a.Hq ? a.q + tok * a.ldq + (int64_t)h * D
-                                   : a.k + tok * a.ldk + (int64_t)(h - a.Hq) * D;
-      raw[u] = *reinterpret_cast<const u32x4*>(p + 8 * l);
-    }
+    if (in && h < H) raw[u] = *reinterpret_cast<const u32x4*>(src + (int64_t)h * D + 8 * l);
   }
 
   // the token's cosines and sines for this lane's elements: pairs, 4 of
@@ -87,21 +112,17 @@ qk_norm_rope_kernel(QkArgs a, int chunks, Gate gate) {
     }
   }
 
-  float w[2][8], b[2][8];
+  float w[8], b[8];
+  const uint16_t* const wp = key ? a.k_w : a.q_w;
+  const uint16_t* const bp = key ? a.k_b : a.q_b;
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const uint16_t* wp = s ? a.k_w : a.q_w;
-    const uint16_t* bp = s ? a.k_b : a.q_b;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[s][i] = 1.0f, b[s][i] = 0.0f;
-    if (wp && in) unpack8(*reinterpret_cast<const u32x4*>(wp + 8 * l), w[s]);
-    if (bp && in) unpack8(*reinterpret_cast<const u32x4*>(bp + 8 * l), b[s]);
-  }
+  for (int i = 0; i < 8; ++i) w[i] = 1.0f, b[i] = 0.0f;
+  if (wp && in) unpack8(*reinterpret_cast<const u32x4*>(wp + 8 * l), w);
+  if (bp && in) unpack8(*reinterpret_cast<const u32x4*>(bp + 8 * l), b);
 
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int h = head0 + u * (64 / LPH);
-    const int s = h < a.Hq ? 0 : 1;
     float x[8];
     unpack8(raw[u], x);
     if (a.norm != QA_NORM_NONE) {
@@ -116,10 +137,9 @@ qk_norm_rope_kernel(QkArgs a, int chunks, Gate gate) {
       float t = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) t = __builtin_fmaf(x[i], x[i], t);
-      const float r = 1.0f / __builtin_sqrtf(head_sum<LPH>(t) * a.inv_D + a.eps);
+      const float r = inverse_sqrt(head_sum<LPH>(t) * a.inv_D + a.eps);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        x[i] = __builtin_fmaf(x[i] * r, s ? w[1][i] : w[0][i], s ? b[1][i] : b[0][i]);
+      for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(x[i] * r, w[i], b[i]);
     }
     if (a.rope == QA_ROPE_PAIRS) {
 #pragma unroll
@@ -137,22 +157,20 @@ qk_norm_rope_kernel(QkArgs a, int chunks, Gate gate) {
         x[i] = __builtin_fmaf(x[i], cs[i], upper ? y * sn[i] : -(y * sn[i]));
       }
     }
-    if (in && h < H) {
-      uint16_t* p = s == 0 ? a.q_out + tok * a.ldqo + (int64_t)h * D
-                           : a.k_out + tok * a.ldko + (int64_t)(h - a.Hq) * D;
-      *reinterpret_cast<u32x4*>(p + 8 * l) = u32x4{bf16_pack(x[0], x[1]), bf16_pack(x[2], x[3]),
-                                                   bf16_pack(x[4], x[5]), bf16_pack(x[6], x[7])};
-    }
+    if (in && h < H)
+      *reinterpret_cast<u32x4*>(dst + (int64_t)h * D + 8 * l) =
+          u32x4{bf16_pack(x[0], x[1]), bf16_pack(x[2], x[3]), bf16_pack(x[4], x[5]),
+                bf16_pack(x[6], x[7])};
   }
 }
 
 template <int LPH>
 hipError_t launch(const QkArgs& a, hipStream_t stream) {
   const int per = 64 / LPH * kQkHeads;
-  const int chunks = (a.Hq + a.Hk + per - 1) / per;
+  const int qchunks = (a.Hq + per - 1) / per, chunks = qchunks + (a.Hk + per - 1) / per;
   const dim3 grid((unsigned)((a.M * chunks + 3) / 4));
-  hipLaunchKernelGGL((qk_norm_rope_kernel<LPH, kQkHeads>), grid, dim3(256), 0, stream, a, chunks,
-                     current_gate());
+  hipLaunchKernelGGL((qk_norm_rope_kernel<LPH, kQkHeads>), grid, dim3(256), 0, stream, a, qchunks,
+                     chunks, current_gate());
   return hipGetLastError();
 }
 
