@@ -380,20 +380,23 @@ def delta_cosine(d_new, d_prev, sums3, ws, n=None, stream=None):
 
 # ------------------------------------ bf16 rows, attention and its inputs --
 
-def _on(dtype, *tensors):
+def _on(dev, dtype, *tensors):
     """Every tensor given (None: not given) is of this dtype, has unit steps
-    in its last dimension and is on the current device."""
-    import torch
-    dev = torch.cuda.current_device()
+    in its last dimension and is on the current device, dev."""
     for t in tensors:
-        if t is None:
-            continue
-        if t.dtype is not dtype and not (dtype is torch.bfloat16 and t.dtype is torch.int16):
-            raise ValueError(f"expected a {dtype} tensor, got {t.dtype}")
-        if t.get_device() != dev:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
-        if not t.is_contiguous() and t.stride(-1) != 1 and t.shape[-1] > 1:
-            raise ValueError("a tensor's last dimension must be contiguous")
+        if t is not None and (t.dtype is not dtype or t.get_device() != dev
+                              or not t.is_contiguous()):
+            _explain(t, dev, dtype)
+
+
+def _explain(t, dev, dtype):
+    import torch
+    if t.dtype is not dtype and not (dtype is torch.bfloat16 and t.dtype is torch.int16):
+        raise ValueError(f"expected a {dtype} tensor, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+    if not t.is_contiguous() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError("a tensor's last dimension must be contiguous")
 
 
 def _whole(*tensors):
@@ -419,10 +422,11 @@ def qlinear_bf16(x, w_q, w_s, w_ts, y, M, N, K, bias=None, out=OUT_BF16, epi=EPI
                  ldy=None, stream=None):
     """The linear of M <= ROWS_MAX bf16 rows x [M, ldx] against an NVFP4 weight."""
     import torch
-    _on(torch.bfloat16, x, bias)
-    _on(torch.uint8, w_q, w_s)
-    _on(torch.float32, w_ts)
-    _on(torch.float32 if out == OUT_F32 else torch.bfloat16, y)
+    dev = torch.cuda.current_device()
+    _on(dev, torch.bfloat16, x, bias)
+    _on(dev, torch.uint8, w_q, w_s)
+    _on(dev, torch.float32, w_ts)
+    _on(dev, torch.float32 if out == OUT_F32 else torch.bfloat16, y)
     ldx = _rows(x, M, K, "x") if ldx is None else ldx
     ldy = max(y.stride(0), y.shape[1]) if ldy is None else ldy
     _check("qlinear_bf16", lib().qlinear_bf16(
@@ -437,9 +441,10 @@ def qk_norm_rope(q, k, q_out, k_out, M, Hq, Hk, D, norm=NORM_LAYER, q_w=None, q_
     float32 tables cos, sin [P, D / 2] at row pos[m] (int32; None: m; outside
     the table: not turned) into q_out and k_out, which may be q and k."""
     import torch
-    _on(torch.bfloat16, q, k, q_out, k_out, q_w, q_b, k_w, k_b)
-    _on(torch.float32, cos, sin)
-    _on(torch.int32, pos)
+    dev = torch.cuda.current_device()
+    _on(dev, torch.bfloat16, q, k, q_out, k_out, q_w, q_b, k_w, k_b)
+    _on(dev, torch.float32, cos, sin)
+    _on(dev, torch.int32, pos)
     ld = [_rows(t, M, h * D, n) if t is not None else 0
           for t, h, n in ((q, Hq, "q"), (k, Hk, "k"), (q_out, Hq, "q_out"), (k_out, Hk, "k_out"))]
     for t in (q_w, q_b, k_w, k_b):
@@ -455,22 +460,22 @@ def qk_norm_rope(q, k, q_out, k_out, M, Hq, Hk, D, norm=NORM_LAYER, q_w=None, q_
         _ptr(k_out), ld[3], _stream(stream)))
 
 
-def _kv4(k_q, k_s, v_q, v_s, k_ts, v_ts, table, B):
+def _kv4(dev, k_q, k_s, v_q, v_s, k_ts, v_ts, table, B):
     """(H, D, pages, page, max_pages) of a cache, after its checks."""
     import torch
-    _on(torch.uint8, k_q, k_s, v_q, v_s)
-    _on(torch.float32, k_ts, v_ts)
-    _on(torch.int32, table)
+    _on(dev, torch.uint8, k_q, k_s, v_q, v_s)
+    _on(dev, torch.float32, k_ts, v_ts)
+    _on(dev, torch.int32, table)
     _whole(k_q, k_s, v_q, v_s, table)
-    if k_q.dim() != 4 or table.dim() != 2:
+    shape, tables = k_q.shape, table.shape
+    if len(shape) != 4 or len(tables) != 2:
         raise ValueError("a cache part is [pages, H, page, D / 2], a table [B, max_pages]")
-    pages, H, page, half = k_q.shape
-    D = 2 * half
-    if v_q.shape != k_q.shape or k_s.shape != (pages, H, page, D // 16) or v_s.shape != k_s.shape:
+    pages, H, page, half = shape
+    if v_q.shape != shape or k_s.shape != (pages, H, page, half // 8) or v_s.shape != k_s.shape:
         raise ValueError("the cache parts' shapes do not fit each other")
-    if table.shape[0] < B:
-        raise ValueError(f"table: needs {B} rows, got {table.shape[0]}")
-    return H, D, pages, page, table.shape[1]
+    if tables[0] < B:
+        raise ValueError(f"table: needs {B} rows, got {tables[0]}")
+    return H, 2 * half, pages, page, tables[1]
 
 
 def kv4_append(k, v, k_q, k_s, v_q, v_s, k_ts, v_ts, table, start, B, T, count=None, stream=None):
@@ -478,9 +483,10 @@ def kv4_append(k, v, k_q, k_s, v_q, v_s, k_ts, v_ts, table, start, B, T, count=N
     the NVFP4 cache at positions start[b] .. start[b] + count[b] - 1 (int32;
     count None: T)."""
     import torch
-    H, D, pages, page, mp = _kv4(k_q, k_s, v_q, v_s, k_ts, v_ts, table, B)
-    _on(torch.bfloat16, k, v)
-    _on(torch.int32, start, count)
+    dev = torch.cuda.current_device()
+    H, D, pages, page, mp = _kv4(dev, k_q, k_s, v_q, v_s, k_ts, v_ts, table, B)
+    _on(dev, torch.bfloat16, k, v)
+    _on(dev, torch.int32, start, count)
     _sized(start, B, "start")
     _sized(count, B, "count")
     _check("kv4_append", lib().kv4_append(
@@ -492,9 +498,10 @@ def kv4_append(k, v, k_q, k_s, v_q, v_s, k_ts, v_ts, table, start, B, T, count=N
 def kv4_read(k, v, k_q, k_s, v_q, v_s, k_ts, v_ts, table, start, B, T, count=None, stream=None):
     """Decode the positions that kv4_append would write into k and v (bf16)."""
     import torch
-    H, D, pages, page, mp = _kv4(k_q, k_s, v_q, v_s, k_ts, v_ts, table, B)
-    _on(torch.bfloat16, k, v)
-    _on(torch.int32, start, count)
+    dev = torch.cuda.current_device()
+    H, D, pages, page, mp = _kv4(dev, k_q, k_s, v_q, v_s, k_ts, v_ts, table, B)
+    _on(dev, torch.bfloat16, k, v)
+    _on(dev, torch.int32, start, count)
     _sized(start, B, "start")
     _sized(count, B, "count")
     _check("kv4_read", lib().kv4_read(
@@ -513,12 +520,13 @@ def attn_kv4(q, k_q, k_s, v_q, v_s, k_ts, v_ts, table, lens, o, B, Lq, Hq, q_len
     first lens[b] positions of each stream's NVFP4 cache into o; scale None:
     1 / sqrt(D)."""
     import torch
-    H, D, pages, page, mp = _kv4(k_q, k_s, v_q, v_s, k_ts, v_ts, table, B)
-    _on(torch.bfloat16, q, o)
-    _on(torch.int32, lens, q_lens)
+    dev = torch.cuda.current_device()
+    H, D, pages, page, mp = _kv4(dev, k_q, k_s, v_q, v_s, k_ts, v_ts, table, B)
+    _on(dev, torch.bfloat16, q, o)
+    _on(dev, torch.int32, lens, q_lens)
     _sized(lens, B, "lens")
     _sized(q_lens, B, "q_lens")
-    _on(torch.uint8, ws)
+    _on(dev, torch.uint8, ws)
     _check("attn_kv4", lib().attn_kv4(
         _ptr(q), _rows(q, B * Lq, Hq * D, "q"), B, Lq, Hq, H, D, _ptr(k_q), _ptr(k_s), _ptr(v_q),
         _ptr(v_s), _ptr(k_ts), _ptr(v_ts), pages, page, _ptr(table), mp, _ptr(lens),
@@ -537,11 +545,12 @@ def attn_cross(q, k, v, o, B, Lq, Lk, Hq, Hkv, D, k_lens=None, mask=None, scale=
     k_lens[b] (int32) with mask[b][j] != 0 (uint8 or bool [B, Lk]); scale
     None: 1 / sqrt(D)."""
     import torch
+    dev = torch.cuda.current_device()
     if mask is not None and mask.dtype == torch.bool:
         mask = mask.view(torch.uint8)
-    _on(torch.bfloat16, q, k, v, o)
-    _on(torch.int32, k_lens)
-    _on(torch.uint8, mask, ws)
+    _on(dev, torch.bfloat16, q, k, v, o)
+    _on(dev, torch.int32, k_lens)
+    _on(dev, torch.uint8, mask, ws)
     _whole(mask)
     _sized(k_lens, B, "k_lens")
     _sized(mask, B * Lk, "mask")
