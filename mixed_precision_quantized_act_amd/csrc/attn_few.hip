@@ -416,35 +416,57 @@ attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gat
   }
 }
 
-// Join the splits of a row: one wave per row, the splits in order.
+// Join the splits of a row, in order, kJoinTurn of them read at a time; D / 4
+// lanes per row.  (512 rows of 128 in 8 splits: one split at a time 8.6 us.)
+constexpr int kJoinTurn = 4;
+
 template <class Source, int D>
 __global__ void __launch_bounds__(256)
 attn_join_kernel(AttnArgs a, Source src, AttnSplit sp, int splits, Gate gate) {
   if (gated_off(gate)) return;
-  const int lane = threadIdx.x & 63;
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);   // (b Lq + t) Hq + head
+  constexpr int kLanes = D / 4, kRows = 256 / kLanes;
+  const int d = 4 * (threadIdx.x % kLanes);
+  const int64_t at = (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes;  // (b Lq + t) Hq + head
   if (at >= sp.rows) return;
-  const int64_t qrow = at / a.Hq, b = qrow / a.Lq;
-  if (qrow - b * a.Lq >= src.queries(b, a.Lq)) return;
-  float mt = -INFINITY;
-  for (int s = 0; s < splits; ++s) mt = fmaxf(mt, sp.m[s * sp.rows + at]);
-  const float ref = mt == -INFINITY ? 0.0f : mt;
-  constexpr int E = D / 64;
-  float l = 0.0f, o[E] = {};
-  for (int s = 0; s < splits; ++s) {
-    const int64_t i = s * sp.rows + at;
-    const float ms = sp.m[i];
-    const float f = ms == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ms - ref);
-    l = __builtin_fmaf(sp.l[i], f, l);
+  const uint32_t qrow = (uint32_t)at / a.Hq, b = qrow / (uint32_t)a.Lq;   // (below 2^24)
+  if ((int)(qrow - b * (uint32_t)a.Lq) >= src.queries(b, a.Lq)) return;
+  float mt = -INFINITY, l = 0.0f;
+  f32x4 o = {0, 0, 0, 0};
+  for (int s0 = 0; s0 < splits; s0 += kJoinTurn) {
+    float ms[kJoinTurn], ls[kJoinTurn];
+    f32x4 os[kJoinTurn];
+    float top = mt;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(sp.o[i * D + E * lane + e], f, o[e]);
+    for (int j = 0; j < kJoinTurn; ++j) {
+      ms[j] = -INFINITY;
+      ls[j] = 0.0f;
+      os[j] = f32x4{0, 0, 0, 0};
+      if (s0 + j < splits) {
+        const int64_t i = (s0 + j) * sp.rows + at;
+        ms[j] = sp.m[i];
+        ls[j] = sp.l[i];
+        os[j] = *reinterpret_cast<const f32x4*>(sp.o + i * D + d);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kJoinTurn; ++j) top = fmaxf(top, ms[j]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    const float f = mt == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mt - ref);
+    mt = top;
+    l *= f;
+    o *= f;
+#pragma unroll
+    for (int j = 0; j < kJoinTurn; ++j) {
+      // (times zero, not left out: a sum that is NaN stays so)
+      const float fj = ms[j] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ms[j] - ref);
+      l = __builtin_fmaf(ls[j], fj, l);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(os[j][e], fj, o[e]);
+    }
   }
   const float f = l == 0.0f ? 0.0f : src.v_scale() / l;
-  uint16_t* dst = a.o + qrow * a.ldo + (at - qrow * a.Hq) * D + E * lane;
-  if constexpr (E == 2)
-    *reinterpret_cast<uint32_t*>(dst) = bf16_pack(o[0] * f, o[1] * f);
-  else
-    *dst = (uint16_t)bf16_pack(o[0] * f, 0.0f);
+  *reinterpret_cast<u32x2*>(a.o + qrow * a.ldo + (int64_t)((uint32_t)at - qrow * a.Hq) * D + d) =
+      u32x2{bf16_pack(o[0] * f, o[1] * f), bf16_pack(o[2] * f, o[3] * f)};
 }
 
 // Workgroups to aim for: a few for each of the 256 CUs, so that streams of
@@ -499,7 +521,8 @@ hipError_t launch_attn_few(const AttnArgs& a, const Source& src, int64_t L, void
 template <class Source>
 hipError_t launch_attn_join(const AttnArgs& a, const Source& src, const AttnSplit& sp, int splits,
                             hipStream_t stream) {
-  const dim3 grid((unsigned)((sp.rows + 3) / 4));
+  const int per = 256 / (a.D / 4);
+  const dim3 grid((unsigned)((sp.rows + per - 1) / per));
   if (a.D == 64)
     hipLaunchKernelGGL((attn_join_kernel<Source, 64>), grid, dim3(256), 0, stream, a, src, sp,
                        splits, current_gate());
