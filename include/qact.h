@@ -405,7 +405,8 @@ int delta_cosine(const uint16_t* d_new, const uint16_t* d_prev, int64_t n, doubl
  * qlinear_nvfp4.  0 <= M <= QA_ROWS_MAX (QA_ESHAPE otherwise: quantize more
  * rows and use qlinear_nvfp4 or qlinear_int8); N, K as there.  Products of
  * a value and a 4-bit element are exact and summed in float32; a group's
- * scale is applied to the sum of its 16 products.  The weight's group
+ * scale is applied to the sum of its 16 products (at most 8 rows) or to the
+ * element (more rows; exact too).  The weight's group
  * scales must be numbers (codes 0x00..0x7E, as act_quant writes them).  No workspace. */
 #define QA_ROWS_MAX 32
 int qlinear_bf16(const uint16_t* x, int64_t ldx, const uint8_t* w_q, const uint8_t* w_s,
@@ -462,7 +463,8 @@ int qk_norm_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int6
  *   of 8, finite values) at positions start[b] .. start[b] + count[b] - 1
  *   (int32 [B]; count NULL: T; the rows behind count[b] are not read).  The
  *   bytes are those of act_quant with QA_TSCALE_GIVEN.  Tokens without a slot
- *   are dropped; every other slot stays as it was.
+ *   are dropped; every other slot stays as it was.  Two tokens of a call that
+ *   have the same slot leave a mix of both there.
  * kv4_read decodes the same positions into k, v (rows behind count[b] and
  *   tokens without a slot are left as they were).
  *   0 <= B, T; B T < 2^24; B T H D < 2^34.
@@ -479,7 +481,9 @@ int qk_norm_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int6
  *   D 64 or 128; Hq a multiple of H; scale > 0; B Lq Hq < 2^24.
  *   ws: with attn_kv4_workspace() bytes a call with few query rows splits
  *   the keys over more workgroups; less (also none) splits less.  The sums
- *   are made in an order that the sizes and ws_bytes decide.
+ *   are made in an order that the sizes and ws_bytes decide.  Calls (and
+ *   replayed graphs) that may run at the same time need workspaces of their
+ *   own; calls in order on one stream may share one.
  * ------------------------------------------------------------------------ */
 int kv4_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, int64_t B,
                int64_t T, int H, int D, uint8_t* k_q, uint8_t* k_s, uint8_t* v_q, uint8_t* v_s,

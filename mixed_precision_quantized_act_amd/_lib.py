@@ -405,12 +405,13 @@ def _whole(*tensors):
             raise ValueError("a cache, table or table-like tensor must be contiguous")
 
 
-def _rows(t, rows, width, name):
-    """Row stride of a 2-D tensor of at least rows x width elements."""
+def _rows(t, rows, width, name, step=8):
+    """Row stride of a 2-D tensor of at least rows x width elements (of a
+    single row: its width, in whole `step`s)."""
     shape = t.shape
     if len(shape) != 2 or shape[0] < rows or shape[1] < width:
         raise ValueError(f"{name}: needs shape [{rows}, {width}], got {tuple(shape)}")
-    return t.stride(0) if shape[0] > 1 else max(t.stride(0), (shape[1] + 7) // 8 * 8)
+    return t.stride(0) if shape[0] > 1 else max(t.stride(0), (shape[1] + step - 1) // step * step)
 
 
 def _sized(t, n, name):
@@ -427,8 +428,13 @@ def qlinear_bf16(x, w_q, w_s, w_ts, y, M, N, K, bias=None, out=OUT_BF16, epi=EPI
     _on(dev, torch.uint8, w_q, w_s)
     _on(dev, torch.float32, w_ts)
     _on(dev, torch.float32 if out == OUT_F32 else torch.bfloat16, y)
+    _whole(w_q, w_s)
+    _sized(w_q, N * K // 2, "w_q")
+    _sized(w_s, N * K // 16, "w_s")
+    _sized(w_ts, 1, "w_ts")
+    _sized(bias, N, "bias")
     ldx = _rows(x, M, K, "x") if ldx is None else ldx
-    ldy = max(y.stride(0), y.shape[1]) if ldy is None else ldy
+    ldy = _rows(y, M, N, "y", 1) if ldy is None else ldy
     _check("qlinear_bf16", lib().qlinear_bf16(
         _ptr(x), ldx, _ptr(w_q), _ptr(w_s), _ptr(w_ts), M, N, K, _ptr(bias), _ptr(y), ldy, out,
         epi, _stream(stream)))
@@ -453,7 +459,9 @@ def qk_norm_rope(q, k, q_out, k_out, M, Hq, Hk, D, norm=NORM_LAYER, q_w=None, q_
     _whole(cos, sin, pos)
     P = 0
     if cos is not None and sin is not None:
-        P = min(cos.numel(), sin.numel()) // (D // 2)
+        if cos.dim() != 2 or cos.shape != sin.shape or cos.shape[1] != D // 2:
+            raise ValueError(f"cos, sin: need shape [P, {D // 2}], got {tuple(cos.shape)}, {tuple(sin.shape)}")
+        P = cos.shape[0]
     _check("qk_norm_rope", lib().qk_norm_rope(
         _ptr(q), ld[0], Hq, _ptr(k), ld[1], Hk, M, D, norm, _ptr(q_w), _ptr(q_b), _ptr(k_w),
         _ptr(k_b), eps, rope, _ptr(cos), _ptr(sin), P, _ptr(pos), _ptr(q_out), ld[2],
@@ -467,6 +475,8 @@ def _kv4(dev, k_q, k_s, v_q, v_s, k_ts, v_ts, table, B):
     _on(dev, torch.float32, k_ts, v_ts)
     _on(dev, torch.int32, table)
     _whole(k_q, k_s, v_q, v_s, table)
+    _sized(k_ts, 1, "k_ts")
+    _sized(v_ts, 1, "v_ts")
     shape, tables = k_q.shape, table.shape
     if len(shape) != 4 or len(tables) != 2:
         raise ValueError("a cache part is [pages, H, page, D / 2], a table [B, max_pages]")
@@ -553,7 +563,8 @@ def attn_cross(q, k, v, o, B, Lq, Lk, Hq, Hkv, D, k_lens=None, mask=None, scale=
     _on(dev, torch.uint8, mask, ws)
     _whole(mask)
     _sized(k_lens, B, "k_lens")
-    _sized(mask, B * Lk, "mask")
+    if mask is not None and (mask.dim() != 2 or mask.shape[0] < B or mask.shape[1] != Lk):
+        raise ValueError(f"mask: needs shape [{B}, {Lk}], got {tuple(mask.shape)}")
     w = Hkv * D
     _check("attn_cross", lib().attn_cross(
         _ptr(q), _rows(q, B * Lq, Hq * D, "q"), _ptr(k), _rows(k, B * Lk, w, "k"), _ptr(v),

@@ -922,7 +922,7 @@ int attn_kv4(const uint16_t* q, int64_t ldq, int64_t B, int64_t Lq, int Hq, int 
 }
 
 size_t attn_cross_workspace(int64_t B, int64_t Lq, int64_t Lk, int Hq, int Hkv, int D) {
-  return attn_sizes(B, Lq, Hq, Hkv, D, Lk) ? attn_ws_bytes(B, Lq, Hq, Hkv, D, Lk) : 0;
+  return attn_sizes(B, Lq, Hq, Hkv, D, Lk) ? attn_cross_ws_bytes(B, Lq, Hq, Hkv, D, Lk) : 0;
 }
 
 int attn_cross(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v,

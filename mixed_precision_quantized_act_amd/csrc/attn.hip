@@ -29,6 +29,10 @@ size_t attn_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
   return attn_few_ws_bytes(B, Lq, Hq, Hkv, D, L);
 }
 
+size_t attn_cross_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t Lk) {
+  return attn_short_takes(B, Lq, Hq, Hkv, Lk) ? 0 : attn_ws_bytes(B, Lq, Hq, Hkv, D, Lk);
+}
+
 hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4Cache& c, const int32_t* lens,
                            const int32_t* q_lens, bool causal, void* ws, size_t ws_bytes,
                            hipStream_t stream) {

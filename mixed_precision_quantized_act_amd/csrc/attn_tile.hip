@@ -364,8 +364,9 @@ Pieces pieces_of(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L, size_
 
 }  // namespace
 
+// (asked for: at most 32 MiB, whatever more pieces would give)
 size_t attn_tile_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
-  const Pieces p = pieces_of(B, Lq, Hq, Hkv, D, L, (size_t)1 << 40);
+  const Pieces p = pieces_of(B, Lq, Hq, Hkv, D, L, (size_t)32 << 20);
   return p.n > 1 ? p.n * AttnSplit::bytes(B * Lq * Hq, D) : 0;
 }
 

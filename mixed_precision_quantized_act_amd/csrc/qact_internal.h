@@ -202,6 +202,7 @@ struct AttnArgs {
 };
 // the workspace that lets a call with few rows split the keys, keys <= L
 size_t attn_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L);
+size_t attn_cross_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t Lk);
 hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4Cache& c, const int32_t* lens,
                            const int32_t* q_lens, bool causal, void* ws, size_t ws_bytes,
                            hipStream_t stream);

@@ -242,3 +242,39 @@ def test_tensors_that_are_refused():
         qa.attn_cross(q, kv, kv, q, 1, 1, 30, 2, 2, 64, ws=q.view(t.uint8)[0])
     t.cuda.synchronize()
     assert (o == 7.0).all()
+
+
+def test_linear_and_norm_tensors_that_are_refused():
+    qa, t = _qa(), torch()
+    x, y = (t.zeros((3, n), dtype=t.bfloat16, device="cuda") for n in (64, 32))
+    wq, ws = (t.zeros((32, n), dtype=t.uint8, device="cuda") for n in (32, 4))
+    ts, b = t.ones(1, device="cuda"), t.zeros(32, dtype=t.bfloat16, device="cuda")
+
+    def rows(**c):
+        a = dict(x=x, w_q=wq, w_s=ws, w_ts=ts, y=y, bias=b)
+        a.update(c)
+        qa.qlinear_bf16(a["x"], a["w_q"], a["w_s"], a["w_ts"], a["y"], 3, 32, 64, bias=a["bias"])
+
+    cos = t.ones((3, 32), device="cuda")
+
+    def norm(**c):
+        a = dict(q=x, q_out=t.empty_like(x), cos=cos, sin=cos.clone(), pos=None, q_w=None)
+        a.update(c)
+        qa.qk_norm_rope(a["q"], None, a["q_out"], None, 3, 1, 0, 64, q_w=a["q_w"], rope=qa.ROPE_PAIRS, cos=a["cos"],
+                        sin=a["sin"], pos=a["pos"])
+
+    rows(), norm()
+    pos = t.zeros(2, dtype=t.int32, device="cuda")
+    wrong = [
+        lambda: rows(x=x[:2]), lambda: rows(x=x[:, :32]), lambda: rows(x=x.float()), lambda: rows(x=x.cpu()),
+        lambda: rows(w_q=wq[:31]), lambda: rows(w_q=wq.t()), lambda: rows(w_s=ws[:, :3]), lambda: rows(w_s=ws.cpu()),
+        lambda: rows(w_ts=ts[:0]), lambda: rows(w_ts=ts.double()), lambda: rows(bias=b[:31]),
+        lambda: rows(y=y[:2]), lambda: rows(y=y[:, :31]), lambda: rows(y=y.float()),
+        lambda: norm(q=x[:2]), lambda: norm(q_out=x[:, :32]), lambda: norm(cos=cos[:2]), lambda: norm(cos=cos.half()),
+        lambda: norm(cos=t.ones((3, 64), device="cuda"), sin=t.ones((3, 64), device="cuda")),
+        lambda: norm(pos=pos), lambda: norm(pos=pos.long()), lambda: norm(q_w=b),
+    ]
+    for i, f in enumerate(wrong):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"call {i} was not refused")
