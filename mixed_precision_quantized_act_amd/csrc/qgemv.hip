@@ -29,9 +29,14 @@
 // against 1920: 12.8, 15.8 and 23.8 us): as many as leave each of the 256
 // compute units one.
 //
+// Against few weight rows the activations are what a compute unit reads most
+// of, so their rows are then shared out as well, 8 or 16 to a workgroup (16 rows
+// of 7680 against 1920: 12.9 us whole, 10.5 in eights; 32 rows of 4096 against
+// 1024: 13.2 and 7.3), as long as all workgroups run at once (16 rows of 4096
+// against 4096: 9.0 and 12.4 us).
+//
 // 1 row, 8192 to 16384: 20.8 us, 3.6 TB/s of the 5.1 that a copy reaches, with
-// the launch; 16 rows, 7680 to 1920: 12.8 us, 120 workgroups that wait for four
-// steps of memory each.
+// the launch.
 #include "qact_device.h"
 #include "qact_internal.h"
 #include "qgemm_common.h"
@@ -108,6 +113,14 @@ __device__ __forceinline__ void finish(const GemvArgs& a, const float (*red)[ROW
   }
 }
 
+// The workgroup's rows of the call's: `most` from blockIdx.y.
+__device__ __forceinline__ void own_rows(GemvArgs& a, int most) {
+  const int64_t first = most * (int64_t)blockIdx.y;
+  a.x += first * a.ldx;
+  a.y = static_cast<char*>(a.y) + first * a.ldy * (a.out_f32 ? 4 : 2);
+  a.M = min(most, a.M - (int)first);
+}
+
 // At most 8 activation rows.  A lane reads pieces of 16 bytes (two groups) of a
 // weight row, lane groups 0 and 1 the even and odd ones of the step's first
 // half, 2 and 3 of its second.  Swapping the odd lane groups' first register
@@ -119,6 +132,7 @@ template <int NR, int RT, int W>
 __global__ void __launch_bounds__(64 * W)
 qgemv_kernel(GemvArgs a, Gate gate) {
   if (gated_off(gate)) return;
+  own_rows(a, 8);
   const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4, up = g >> 1;
@@ -249,6 +263,7 @@ template <int MT, int RT, int W>
 __global__ void __launch_bounds__(64 * W)
 qgemv_wide_kernel(GemvArgs a, Gate gate) {
   if (gated_off(gate)) return;
+  own_rows(a, 16 * MT);
   const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
@@ -379,16 +394,21 @@ template <int RT>
 hipError_t launch(const GemvArgs& a, hipStream_t stream) {
   constexpr int W = kGvWaves;
   const int64_t nsteps = (a.K + kGvStep - 1) / kGvStep;
-  const dim3 grid((unsigned)((a.N + kGvRows * RT - 1) / (kGvRows * RT)));
+  const int64_t tiles = (a.N + kGvRows * RT - 1) / (kGvRows * RT);
+  // activation rows of a workgroup: 8, 16 or 32, the fewest that leave one
+  // workgroup for each compute unit or make all of them one
+  int most = 8;
+  while (most < a.M && tiles * ((a.M + most - 1) / most) > kGvPlaces) most *= 2;
+  const dim3 grid((unsigned)tiles, (unsigned)((a.M + most - 1) / most));
   const dim3 block((unsigned)(64 * (nsteps < W ? nsteps : W)));
   const Gate gt = current_gate();
   if (a.M <= 2)
     hipLaunchKernelGGL((qgemv_kernel<1, RT, W>), grid, block, 0, stream, a, gt);
   else if (a.M <= 4)
     hipLaunchKernelGGL((qgemv_kernel<2, RT, W>), grid, block, 0, stream, a, gt);
-  else if (a.M <= 8)
+  else if (most == 8)
     hipLaunchKernelGGL((qgemv_kernel<4, RT, W>), grid, block, 0, stream, a, gt);
-  else if (a.M <= 16)
+  else if (most == 16)
     hipLaunchKernelGGL((qgemv_wide_kernel<1, RT, W>), grid, block, 0, stream, a, gt);
   else
     hipLaunchKernelGGL((qgemv_wide_kernel<2, RT, W>), grid, block, 0, stream, a, gt);

@@ -55,3 +55,12 @@ def test_norm_of_tiny_heads_without_eps(exponent, norm):
     # values of at most sqrt(D) deviations
     tol = U_BF16 * np.abs(y) + 4 * (D + 16) * U_F32 * np.sqrt(D)
     assert np.all(np.abs(val(host(o)).reshape(M, H, D) - y) <= tol)
+
+
+@pytest.mark.parametrize("N", [1, 510, 1024, 1030, 2050, 2064, 4096, 4100])
+@pytest.mark.parametrize("M", [8, 9, 15, 16, 17, 24, 25, 31, 32])
+def test_rows_shared_out_over_workgroups(M, N):
+    """8, 16 or 32 rows to a workgroup, by the weight's size; bf16 rows of a wider output."""
+    x, w, b = _case(M, N, 288, 14)
+    y, e = _expect(x, w, b, False)
+    _close(_call(x, w, N, 288, b, False, ldx=296, ldy=N + 3), y, e, False)
