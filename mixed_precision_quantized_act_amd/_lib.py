@@ -141,8 +141,16 @@ def _stream(stream):
     if stream is not None:
         return stream
     import torch
-    # (the handle alone: building a torch.cuda.Stream takes 3 us a call)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return _current(None, torch.cuda.current_device())
+
+
+def _current(stream, dev):
+    """The stream given, or device dev's current one (its handle alone:
+    building a torch.cuda.Stream takes 3 us a call)."""
+    if stream is not None:
+        return stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _nbytes(t):
@@ -389,6 +397,16 @@ def _on(dev, dtype, *tensors):
             _explain(t, dev, dtype)
 
 
+def _solid(dev, dtype, *tensors):
+    """The same of tensors that must be contiguous in all dimensions."""
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.get_device() != dev
+                              or not t.is_contiguous()):
+            _explain(t, dev, dtype)
+            if not t.is_contiguous():
+                raise ValueError("a cache, table, weight or mask must be contiguous")
+
+
 def _explain(t, dev, dtype):
     import torch
     if t.dtype is not dtype and not (dtype is torch.bfloat16 and t.dtype is torch.int16):
@@ -397,12 +415,6 @@ def _explain(t, dev, dtype):
         raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
     if not t.is_contiguous() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError("a tensor's last dimension must be contiguous")
-
-
-def _whole(*tensors):
-    for t in tensors:
-        if t is not None and not t.is_contiguous():
-            raise ValueError("a cache, table or table-like tensor must be contiguous")
 
 
 def _rows(t, rows, width, name, step=8):
@@ -425,10 +437,9 @@ def qlinear_bf16(x, w_q, w_s, w_ts, y, M, N, K, bias=None, out=OUT_BF16, epi=EPI
     import torch
     dev = torch.cuda.current_device()
     _on(dev, torch.bfloat16, x, bias)
-    _on(dev, torch.uint8, w_q, w_s)
+    _solid(dev, torch.uint8, w_q, w_s)
     _on(dev, torch.float32, w_ts)
     _on(dev, torch.float32 if out == OUT_F32 else torch.bfloat16, y)
-    _whole(w_q, w_s)
     _sized(w_q, N * K // 2, "w_q")
     _sized(w_s, N * K // 16, "w_s")
     _sized(w_ts, 1, "w_ts")
@@ -437,7 +448,7 @@ def qlinear_bf16(x, w_q, w_s, w_ts, y, M, N, K, bias=None, out=OUT_BF16, epi=EPI
     ldy = _rows(y, M, N, "y", 1) if ldy is None else ldy
     _check("qlinear_bf16", lib().qlinear_bf16(
         _ptr(x), ldx, _ptr(w_q), _ptr(w_s), _ptr(w_ts), M, N, K, _ptr(bias), _ptr(y), ldy, out,
-        epi, _stream(stream)))
+        epi, _current(stream, dev)))
 
 
 def qk_norm_rope(q, k, q_out, k_out, M, Hq, Hk, D, norm=NORM_LAYER, q_w=None, q_b=None, k_w=None,
@@ -449,14 +460,13 @@ def qk_norm_rope(q, k, q_out, k_out, M, Hq, Hk, D, norm=NORM_LAYER, q_w=None, q_
     import torch
     dev = torch.cuda.current_device()
     _on(dev, torch.bfloat16, q, k, q_out, k_out, q_w, q_b, k_w, k_b)
-    _on(dev, torch.float32, cos, sin)
-    _on(dev, torch.int32, pos)
+    _solid(dev, torch.float32, cos, sin)
+    _solid(dev, torch.int32, pos)
     ld = [_rows(t, M, h * D, n) if t is not None else 0
           for t, h, n in ((q, Hq, "q"), (k, Hk, "k"), (q_out, Hq, "q_out"), (k_out, Hk, "k_out"))]
     for t in (q_w, q_b, k_w, k_b):
         _sized(t, D, "a norm's weight or bias")
     _sized(pos, M, "pos")
-    _whole(cos, sin, pos)
     P = 0
     if cos is not None and sin is not None:
         if cos.dim() != 2 or cos.shape != sin.shape or cos.shape[1] != D // 2:
@@ -465,16 +475,15 @@ def qk_norm_rope(q, k, q_out, k_out, M, Hq, Hk, D, norm=NORM_LAYER, q_w=None, q_
     _check("qk_norm_rope", lib().qk_norm_rope(
         _ptr(q), ld[0], Hq, _ptr(k), ld[1], Hk, M, D, norm, _ptr(q_w), _ptr(q_b), _ptr(k_w),
         _ptr(k_b), eps, rope, _ptr(cos), _ptr(sin), P, _ptr(pos), _ptr(q_out), ld[2],
-        _ptr(k_out), ld[3], _stream(stream)))
+        _ptr(k_out), ld[3], _current(stream, dev)))
 
 
 def _kv4(dev, k_q, k_s, v_q, v_s, k_ts, v_ts, table, B):
     """(H, D, pages, page, max_pages) of a cache, after its checks."""
     import torch
-    _on(dev, torch.uint8, k_q, k_s, v_q, v_s)
+    _solid(dev, torch.uint8, k_q, k_s, v_q, v_s)
     _on(dev, torch.float32, k_ts, v_ts)
-    _on(dev, torch.int32, table)
-    _whole(k_q, k_s, v_q, v_s, table)
+    _solid(dev, torch.int32, table)
     _sized(k_ts, 1, "k_ts")
     _sized(v_ts, 1, "v_ts")
     shape, tables = k_q.shape, table.shape
@@ -502,7 +511,7 @@ def kv4_append(k, v, k_q, k_s, v_q, v_s, k_ts, v_ts, table, start, B, T, count=N
     _check("kv4_append", lib().kv4_append(
         _ptr(k), _rows(k, B * T, H * D, "k"), _ptr(v), _rows(v, B * T, H * D, "v"), B, T, H, D,
         _ptr(k_q), _ptr(k_s), _ptr(v_q), _ptr(v_s), _ptr(k_ts), _ptr(v_ts), pages, page,
-        _ptr(table), mp, _ptr(start), _ptr(count), _stream(stream)))
+        _ptr(table), mp, _ptr(start), _ptr(count), _current(stream, dev)))
 
 
 def kv4_read(k, v, k_q, k_s, v_q, v_s, k_ts, v_ts, table, start, B, T, count=None, stream=None):
@@ -517,7 +526,7 @@ def kv4_read(k, v, k_q, k_s, v_q, v_s, k_ts, v_ts, table, start, B, T, count=Non
     _check("kv4_read", lib().kv4_read(
         _ptr(k), _rows(k, B * T, H * D, "k"), _ptr(v), _rows(v, B * T, H * D, "v"), B, T, H, D,
         _ptr(k_q), _ptr(k_s), _ptr(v_q), _ptr(v_s), _ptr(k_ts), _ptr(v_ts), pages, page,
-        _ptr(table), mp, _ptr(start), _ptr(count), _stream(stream)))
+        _ptr(table), mp, _ptr(start), _ptr(count), _current(stream, dev)))
 
 
 def attn_kv4_workspace(B, Lq, Hq, H, D, max_len):
@@ -536,12 +545,12 @@ def attn_kv4(q, k_q, k_s, v_q, v_s, k_ts, v_ts, table, lens, o, B, Lq, Hq, q_len
     _on(dev, torch.int32, lens, q_lens)
     _sized(lens, B, "lens")
     _sized(q_lens, B, "q_lens")
-    _on(dev, torch.uint8, ws)
+    _solid(dev, torch.uint8, ws)
     _check("attn_kv4", lib().attn_kv4(
         _ptr(q), _rows(q, B * Lq, Hq * D, "q"), B, Lq, Hq, H, D, _ptr(k_q), _ptr(k_s), _ptr(v_q),
         _ptr(v_s), _ptr(k_ts), _ptr(v_ts), pages, page, _ptr(table), mp, _ptr(lens),
         _ptr(q_lens), 1 if causal else 0, D ** -0.5 if scale is None else scale, _ptr(o),
-        _rows(o, B * Lq, Hq * D, "o"), _ptr(ws), _nbytes(ws), _stream(stream)))
+        _rows(o, B * Lq, Hq * D, "o"), _ptr(ws), _nbytes(ws), _current(stream, dev)))
 
 
 def attn_cross_workspace(B, Lq, Lk, Hq, Hkv, D):
@@ -560,8 +569,7 @@ def attn_cross(q, k, v, o, B, Lq, Lk, Hq, Hkv, D, k_lens=None, mask=None, scale=
         mask = mask.view(torch.uint8)
     _on(dev, torch.bfloat16, q, k, v, o)
     _on(dev, torch.int32, k_lens)
-    _on(dev, torch.uint8, mask, ws)
-    _whole(mask)
+    _solid(dev, torch.uint8, mask, ws)
     _sized(k_lens, B, "k_lens")
     if mask is not None and (mask.dim() != 2 or mask.shape[0] < B or mask.shape[1] != Lk):
         raise ValueError(f"mask: needs shape [{B}, {Lk}], got {tuple(mask.shape)}")
@@ -570,7 +578,7 @@ def attn_cross(q, k, v, o, B, Lq, Lk, Hq, Hkv, D, k_lens=None, mask=None, scale=
         _ptr(q), _rows(q, B * Lq, Hq * D, "q"), _ptr(k), _rows(k, B * Lk, w, "k"), _ptr(v),
         _rows(v, B * Lk, w, "v"), B, Lq, Lk, Hq, Hkv, D, _ptr(k_lens), _ptr(mask),
         D ** -0.5 if scale is None else scale, _ptr(o), _rows(o, B * Lq, Hq * D, "o"), _ptr(ws),
-        _nbytes(ws), _stream(stream)))
+        _nbytes(ws), _current(stream, dev)))
 
 
 # ------------------------------------------------------- host decisions --
