@@ -30,7 +30,7 @@ size_t attn_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
 }
 
 size_t attn_cross_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t Lk) {
-  return attn_short_takes(B, Lq, Hq, Hkv, Lk) ? 0 : attn_ws_bytes(B, Lq, Hq, Hkv, D, Lk);
+  return attn_short_takes(Lq, Hq, Hkv, D, Lk) ? 0 : attn_ws_bytes(B, Lq, Hq, Hkv, D, Lk);
 }
 
 hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4Cache& c, const int32_t* lens,
@@ -44,7 +44,7 @@ hipError_t launch_attn_cross(const AttnArgs& a, const uint16_t* k, int64_t ldk, 
                              int64_t ldv, int64_t Lk, const int32_t* k_lens, const uint8_t* mask,
                              void* ws, size_t ws_bytes, hipStream_t stream) {
   const CrossSource src = {k, v, ldk, ldv, (int)Lk, k_lens, mask};
-  if (attn_short_takes(a.B, a.Lq, a.Hq, a.Hkv, Lk)) return launch_attn_short(a, src, stream);
+  if (attn_short_takes(a.Lq, a.Hq, a.Hkv, a.D, Lk)) return launch_attn_short(a, src, stream);
   return launch(a, src, Lk, ws, ws_bytes, stream);
 }
 

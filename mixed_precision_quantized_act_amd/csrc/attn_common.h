@@ -294,7 +294,7 @@ hipError_t launch_attn_tile(const AttnArgs& a, const Source& src, int64_t L, voi
                             size_t ws_bytes, hipStream_t stream);
 
 // Many query rows to few states (attn_short.hip), where it takes the sizes.
-bool attn_short_takes(int64_t B, int64_t Lq, int Hq, int Hkv, int64_t Lk);
+bool attn_short_takes(int64_t Lq, int Hq, int Hkv, int D, int64_t Lk);
 hipError_t launch_attn_short(const AttnArgs& a, const CrossSource& src, hipStream_t stream);
 
 }  // namespace qact

@@ -1,5 +1,5 @@
-// Cross attention to few states (a prompt's): many query rows to at most 256
-// states.  All keys and values of a head lie in shared memory, staged once for
+// Cross attention to few states (a prompt's): many query rows to at most 512
+// states (heads of 64; of 128: 256).  All keys and values of a head lie in shared memory, staged once for
 // a workgroup's whole share of the query rows, and its waves go through their
 // rows, 32 at a time, without meeting again; the next 32 are on their way
 // meanwhile.  attn_rows.h says what a wave does with them.
@@ -17,11 +17,15 @@ namespace qact {
 namespace {
 
 constexpr int kShortWaves = 8;
-constexpr int kShortTiles = 4;
+// Tiles of keys that fit the shared memory.  A kernel of its own for the first
+// four spares those the other tiles' places (226 states: 60 and 61.5 us; 512 states,
+// 8000 tokens: 45 us, 60 in staged tiles).
+template <int D>
+constexpr int kShortTiles = D == 64 ? 8 : 4;
 
 // Workgroup: (sequence and key head, share of the row blocks), the share
 // running fastest.
-template <int D>
+template <int D, int kTiles>
 __global__ void __launch_bounds__(64 * kShortWaves, 2)
 attn_short_kernel(AttnArgs a, CrossSource src, int blocks, int shares, Gate gate) {
   if (gated_off(gate)) return;
@@ -29,10 +33,10 @@ attn_short_kernel(AttnArgs a, CrossSource src, int blocks, int shares, Gate gate
   using R = Rows<false, D>;
   constexpr int kBytes = kTileKeys * D * 2, kHalf = kBytes / 2, kPieces = D / 8;
   // K, V, and half a tile of zeros: the values before the first tile
-  constexpr int kZeros = kShortTiles * kBytes - kHalf;              // (read from + kHalf on)
-  __shared__ __align__(16) char lds[2 * kShortTiles * kBytes + kHalf];
+  constexpr int kZeros = kTiles * kBytes - kHalf;              // (read from + kHalf on)
+  __shared__ __align__(16) char lds[2 * kTiles * kBytes + kHalf];
   char* const kt = lds;
-  char* const vt = lds + kShortTiles * kBytes;
+  char* const vt = lds + kTiles * kBytes;
 
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -55,23 +59,25 @@ attn_short_kernel(AttnArgs a, CrossSource src, int blocks, int shares, Gate gate
   if (block < last) fetch(block);
   // a thread's pieces of the keys; what is not seen may hold NaN and is zeroed
   // when that is known
-  constexpr int kLoads = kShortTiles * kTileKeys * kPieces / (64 * W);
+  constexpr int kLoads = kTiles * kTileKeys * kPieces / (64 * W);
+  constexpr int kOf = kTileKeys * kPieces / (64 * W);           // of a tile
   u32x4 kr[kLoads], vr[kLoads];
 #pragma unroll
   for (int u = 0; u < kLoads; ++u) {
+    if (kTiles > 4 && u / kOf * kTileKeys >= src.Lk) break;
     const int x = u * 64 * W + tid, c = x % kPieces;
-    const int64_t row = b * src.Lk + min((int64_t)(x / kPieces), src.Lk - 1);
+    const int64_t row = b * src.Lk + min(x / kPieces, src.Lk - 1);
     kr[u] = *reinterpret_cast<const u32x4*>(src.k + row * src.ldk + hk * D + 8 * c);
     vr[u] = *reinterpret_cast<const u32x4*>(src.v + row * src.ldv + hk * D + 8 * c);
   }
 
-  uint64_t seen[kShortTiles];
+  uint64_t seen[kTiles];
 #pragma unroll
-  for (int t = 0; t < kShortTiles; ++t)
+  for (int t = 0; t < kTiles; ++t)
     seen[t] = src.seen(src.look(b, t * kTileKeys, n, lane), t * kTileKeys, n, lane);
 #pragma unroll
   for (int u = 0; u < kLoads; ++u) {
-    constexpr int kOf = kTileKeys * kPieces / (64 * W);         // loads of a tile
+    if (kTiles > 4 && u / kOf * kTileKeys >= src.Lk) break;
     const int t = u / kOf, x = u % kOf * 64 * W + tid, key = x / kPieces, c = x % kPieces;
     if (!((seen[t] >> key) & 1)) kr[u] = vr[u] = u32x4{0, 0, 0, 0};
     *reinterpret_cast<u32x4*>(kt + t * kBytes + k_piece<D>(key, c)) = kr[u];
@@ -103,7 +109,9 @@ attn_short_kernel(AttnArgs a, CrossSource src, int blocks, int shares, Gate gate
       for (int g = 0; g < R::kAhead; ++g) ahead[g] = r.template operand<kHalf>(g, kt, ka, vt, va);
 #pragma unroll 1
       for (int t = 0; t < nt; ++t) {
-        const uint64_t here = t < 2 ? (t == 0 ? seen[0] : seen[1]) : (t == 2 ? seen[2] : seen[3]);
+        uint64_t here = t < 2 ? (t == 0 ? seen[0] : seen[1]) : (t == 2 ? seen[2] : seen[3]);
+        if constexpr (kTiles == 8)
+          if (t >= 4) here = t < 6 ? (t == 4 ? seen[4] : seen[5]) : (t == 6 ? seen[6] : seen[7]);
         if ((uint32_t)here != ~0u) hide(s0, (uint32_t)here);
         if (t == 0) r.start(s0);
         r.template step<kHalf, 0>(s0, p0, s1, p1, sum, ahead, kt, ka, vt, va, kBytes,
@@ -126,41 +134,44 @@ attn_short_kernel(AttnArgs a, CrossSource src, int blocks, int shares, Gate gate
   }
 }
 
-// Workgroups that run at once, and the time (us) of staging and of one pass of
-// the waves of each.
+// Workgroups that run at once, and the relative times of staging and of one pass
+// of a workgroup's waves, of it by tile.
 constexpr int64_t kPlaces = 256;
-constexpr double kStage = 3.0, kPass = 3.2;
+constexpr double kStage = 3.0, kPass = 0.8, kPassTile = 0.6;
 
 }  // namespace
 
-bool attn_short_takes(int64_t B, int64_t Lq, int Hq, int Hkv, int64_t Lk) {
-  return Lk >= 1 && Lk <= kShortTiles * kTileKeys && Lq * (Hq / Hkv) >= 256;
+bool attn_short_takes(int64_t Lq, int Hq, int Hkv, int D, int64_t Lk) {
+  return Lk >= 1 && Lk <= (D == 64 ? kShortTiles<64> : kShortTiles<128>) * kTileKeys && Lq * (Hq / Hkv) >= 256;
 }
 
-template <int D>
+template <int D, int kTiles>
 static hipError_t launch(const AttnArgs& a, const CrossSource& src, hipStream_t stream) {
   constexpr int W = kShortWaves;
   const int64_t units = a.B * a.Hkv;
   const int blocks = (int)((a.Lq * (a.Hq / a.Hkv) + 31) / 32);
   // shares of a head's rows: the rounds of workgroups times the passes of each
+  const double pass = kPass + kPassTile * (double)((src.Lk + kTileKeys - 1) / kTileKeys);
   int shares = 1;
   double least = 0.0;
   for (int s = 1; s <= 64 && (s == 1 || s * W <= blocks); ++s) {
     const int64_t rounds = (units * s + kPlaces - 1) / kPlaces;
     const int64_t passes = (blocks + (int64_t)s * W - 1) / ((int64_t)s * W);
-    const double cost = (double)rounds * (kStage + (double)passes * kPass);
+    const double cost = (double)rounds * (kStage + (double)passes * pass);
     if (s == 1 || cost < least) {
       least = cost;
       shares = s;
     }
   }
-  hipLaunchKernelGGL((attn_short_kernel<D>), dim3((unsigned)(units * shares)), dim3(64 * W), 0,
+  hipLaunchKernelGGL((attn_short_kernel<D, kTiles>), dim3((unsigned)(units * shares)), dim3(64 * W), 0,
                      stream, a, src, blocks, shares, current_gate());
   return hipGetLastError();
 }
 
 hipError_t launch_attn_short(const AttnArgs& a, const CrossSource& src, hipStream_t stream) {
-  return a.D == 64 ? launch<64>(a, src, stream) : launch<128>(a, src, stream);
+  if (a.D == 128) return launch<128, kShortTiles<128>>(a, src, stream);
+  return src.Lk <= 4 * kTileKeys ? launch<64, 4>(a, src, stream)
+                                 : launch<64, kShortTiles<64>>(a, src, stream);
 }
 
 }  // namespace qact

@@ -278,3 +278,12 @@ def test_linear_and_norm_tensors_that_are_refused():
         with pytest.raises(ValueError):
             f()
             pytest.fail(f"call {i} was not refused")
+
+
+@pytest.mark.parametrize("Lk", [257, 320, 449, 511, 512, 513])
+@pytest.mark.parametrize("Lq,Hq,H", [(256, 1, 1), (700, 2, 1)])
+def test_cross_more_of_few_states(Lk, Lq, Hq, H):
+    m = rng(804, Lk).random((2, Lk)) < 0.7
+    m[0, 130:] = False
+    _cross(29, 2, Lq, Lk, Hq, H, 64)
+    _cross(29, 2, Lq, Lk, Hq, H, 64, mask=m, k_lens=[Lk, Lk - 100])
