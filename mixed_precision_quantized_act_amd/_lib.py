@@ -141,16 +141,8 @@ def _stream(stream):
     if stream is not None:
         return stream
     import torch
-    return _current(None, torch.cuda.current_device())
-
-
-def _current(stream, dev):
-    """The stream given, or device dev's current one (its handle alone:
-    building a torch.cuda.Stream takes 3 us a call)."""
-    if stream is not None:
-        return stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev)
+    # (the handle alone: building a torch.cuda.Stream takes 3 us a call)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _nbytes(t):
@@ -388,67 +380,32 @@ def delta_cosine(d_new, d_prev, sums3, ws, n=None, stream=None):
 
 # ------------------------------------ bf16 rows, attention and its inputs --
 
-def _on(dev, dtype, *tensors):
-    """Every tensor given (None: not given) is of this dtype, has unit steps
-    in its last dimension and is on the current device, dev."""
-    for t in tensors:
-        if t is not None and (t.dtype is not dtype or t.get_device() != dev
-                              or not t.is_contiguous()):
-            _explain(t, dev, dtype)
+_call = None
 
 
-def _solid(dev, dtype, *tensors):
-    """The same of tensors that must be contiguous in all dimensions."""
-    for t in tensors:
-        if t is not None and (t.dtype is not dtype or t.get_device() != dev
-                              or not t.is_contiguous()):
-            _explain(t, dev, dtype)
-            if not t.is_contiguous():
-                raise ValueError("a cache, table, weight or mask must be contiguous")
-
-
-def _explain(t, dev, dtype):
-    import torch
-    if t.dtype is not dtype and not (dtype is torch.bfloat16 and t.dtype is torch.int16):
-        raise ValueError(f"expected a {dtype} tensor, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
-    if not t.is_contiguous() and t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError("a tensor's last dimension must be contiguous")
-
-
-def _rows(t, rows, width, name, step=8):
-    """Row stride of a 2-D tensor of at least rows x width elements (of a
-    single row: its width, in whole `step`s)."""
-    shape = t.shape
-    if len(shape) != 2 or shape[0] < rows or shape[1] < width:
-        raise ValueError(f"{name}: needs shape [{rows}, {width}], got {tuple(shape)}")
-    return t.stride(0) if shape[0] > 1 else max(t.stride(0), (shape[1] + step - 1) // step * step)
-
-
-def _sized(t, n, name):
-    if t is not None and t.numel() < n:
-        raise ValueError(f"{name}: needs {n} elements, got {t.numel()}")
+def _native():
+    """The compiled calls of the entry points below (they check their tensors
+    and call the library without Python in between)."""
+    global _call
+    if _call is None:
+        h = lib()
+        try:
+            from . import _call as m
+        except ImportError as e:
+            raise ImportError("_call.so is not built (or for another PyTorch); run "
+                              "python -m mixed_precision_quantized_act_amd.build") from e
+        m.bind(*(ctypes.cast(getattr(h, n), ctypes.c_void_p).value for n in (
+            "qlinear_bf16", "qk_norm_rope", "kv4_append", "kv4_read", "attn_kv4", "attn_cross")))
+        _call = m
+    return _call
 
 
 def qlinear_bf16(x, w_q, w_s, w_ts, y, M, N, K, bias=None, out=OUT_BF16, epi=EPI_NONE, ldx=None,
                  ldy=None, stream=None):
     """The linear of M <= ROWS_MAX bf16 rows x [M, ldx] against an NVFP4 weight."""
-    import torch
-    dev = torch.cuda.current_device()
-    _on(dev, torch.bfloat16, x, bias)
-    _solid(dev, torch.uint8, w_q, w_s)
-    _on(dev, torch.float32, w_ts)
-    _on(dev, torch.float32 if out == OUT_F32 else torch.bfloat16, y)
-    _sized(w_q, N * K // 2, "w_q")
-    _sized(w_s, N * K // 16, "w_s")
-    _sized(w_ts, 1, "w_ts")
-    _sized(bias, N, "bias")
-    ldx = _rows(x, M, K, "x") if ldx is None else ldx
-    ldy = _rows(y, M, N, "y", 1) if ldy is None else ldy
-    _check("qlinear_bf16", lib().qlinear_bf16(
-        _ptr(x), ldx, _ptr(w_q), _ptr(w_s), _ptr(w_ts), M, N, K, _ptr(bias), _ptr(y), ldy, out,
-        epi, _current(stream, dev)))
+    status = _native().qlinear_bf16(x, w_q, w_s, w_ts, y, M, N, K, bias, out, epi, ldx, ldy, stream)
+    if status:
+        _check("qlinear_bf16", status)
 
 
 def qk_norm_rope(q, k, q_out, k_out, M, Hq, Hk, D, norm=NORM_LAYER, q_w=None, q_b=None, k_w=None,
@@ -457,76 +414,28 @@ def qk_norm_rope(q, k, q_out, k_out, M, Hq, Hk, D, norm=NORM_LAYER, q_w=None, q_
     (bf16, rows of any stride; None without heads) and their rotation by the
     float32 tables cos, sin [P, D / 2] at row pos[m] (int32; None: m; outside
     the table: not turned) into q_out and k_out, which may be q and k."""
-    import torch
-    dev = torch.cuda.current_device()
-    _on(dev, torch.bfloat16, q, k, q_out, k_out, q_w, q_b, k_w, k_b)
-    _solid(dev, torch.float32, cos, sin)
-    _solid(dev, torch.int32, pos)
-    ld = [_rows(t, M, h * D, n) if t is not None else 0
-          for t, h, n in ((q, Hq, "q"), (k, Hk, "k"), (q_out, Hq, "q_out"), (k_out, Hk, "k_out"))]
-    for t in (q_w, q_b, k_w, k_b):
-        _sized(t, D, "a norm's weight or bias")
-    _sized(pos, M, "pos")
-    P = 0
-    if cos is not None and sin is not None:
-        if cos.dim() != 2 or cos.shape != sin.shape or cos.shape[1] != D // 2:
-            raise ValueError(f"cos, sin: need shape [P, {D // 2}], got {tuple(cos.shape)}, {tuple(sin.shape)}")
-        P = cos.shape[0]
-    _check("qk_norm_rope", lib().qk_norm_rope(
-        _ptr(q), ld[0], Hq, _ptr(k), ld[1], Hk, M, D, norm, _ptr(q_w), _ptr(q_b), _ptr(k_w),
-        _ptr(k_b), eps, rope, _ptr(cos), _ptr(sin), P, _ptr(pos), _ptr(q_out), ld[2],
-        _ptr(k_out), ld[3], _current(stream, dev)))
-
-
-def _kv4(dev, k_q, k_s, v_q, v_s, k_ts, v_ts, table, B):
-    """(H, D, pages, page, max_pages) of a cache, after its checks."""
-    import torch
-    _solid(dev, torch.uint8, k_q, k_s, v_q, v_s)
-    _on(dev, torch.float32, k_ts, v_ts)
-    _solid(dev, torch.int32, table)
-    _sized(k_ts, 1, "k_ts")
-    _sized(v_ts, 1, "v_ts")
-    shape, tables = k_q.shape, table.shape
-    if len(shape) != 4 or len(tables) != 2:
-        raise ValueError("a cache part is [pages, H, page, D / 2], a table [B, max_pages]")
-    pages, H, page, half = shape
-    if v_q.shape != shape or k_s.shape != (pages, H, page, half // 8) or v_s.shape != k_s.shape:
-        raise ValueError("the cache parts' shapes do not fit each other")
-    if tables[0] < B:
-        raise ValueError(f"table: needs {B} rows, got {tables[0]}")
-    return H, 2 * half, pages, page, tables[1]
+    status = _native().qk_norm_rope(q, k, q_out, k_out, M, Hq, Hk, D, norm, q_w, q_b, k_w, k_b, eps,
+                                    rope, cos, sin, pos, stream)
+    if status:
+        _check("qk_norm_rope", status)
 
 
 def kv4_append(k, v, k_q, k_s, v_q, v_s, k_ts, v_ts, table, start, B, T, count=None, stream=None):
     """Encode keys and values (bf16 [B * T, H * D], rows of any stride) into
     the NVFP4 cache at positions start[b] .. start[b] + count[b] - 1 (int32;
     count None: T)."""
-    import torch
-    dev = torch.cuda.current_device()
-    H, D, pages, page, mp = _kv4(dev, k_q, k_s, v_q, v_s, k_ts, v_ts, table, B)
-    _on(dev, torch.bfloat16, k, v)
-    _on(dev, torch.int32, start, count)
-    _sized(start, B, "start")
-    _sized(count, B, "count")
-    _check("kv4_append", lib().kv4_append(
-        _ptr(k), _rows(k, B * T, H * D, "k"), _ptr(v), _rows(v, B * T, H * D, "v"), B, T, H, D,
-        _ptr(k_q), _ptr(k_s), _ptr(v_q), _ptr(v_s), _ptr(k_ts), _ptr(v_ts), pages, page,
-        _ptr(table), mp, _ptr(start), _ptr(count), _current(stream, dev)))
+    status = _native().kv4_append(k, v, k_q, k_s, v_q, v_s, k_ts, v_ts, table, start, B, T, count,
+                                  stream)
+    if status:
+        _check("kv4_append", status)
 
 
 def kv4_read(k, v, k_q, k_s, v_q, v_s, k_ts, v_ts, table, start, B, T, count=None, stream=None):
     """Decode the positions that kv4_append would write into k and v (bf16)."""
-    import torch
-    dev = torch.cuda.current_device()
-    H, D, pages, page, mp = _kv4(dev, k_q, k_s, v_q, v_s, k_ts, v_ts, table, B)
-    _on(dev, torch.bfloat16, k, v)
-    _on(dev, torch.int32, start, count)
-    _sized(start, B, "start")
-    _sized(count, B, "count")
-    _check("kv4_read", lib().kv4_read(
-        _ptr(k), _rows(k, B * T, H * D, "k"), _ptr(v), _rows(v, B * T, H * D, "v"), B, T, H, D,
-        _ptr(k_q), _ptr(k_s), _ptr(v_q), _ptr(v_s), _ptr(k_ts), _ptr(v_ts), pages, page,
-        _ptr(table), mp, _ptr(start), _ptr(count), _current(stream, dev)))
+    status = _native().kv4_read(k, v, k_q, k_s, v_q, v_s, k_ts, v_ts, table, start, B, T, count,
+                                stream)
+    if status:
+        _check("kv4_read", status)
 
 
 def attn_kv4_workspace(B, Lq, Hq, H, D, max_len):
@@ -538,19 +447,10 @@ def attn_kv4(q, k_q, k_s, v_q, v_s, k_ts, v_ts, table, lens, o, B, Lq, Hq, q_len
     """Attention of q [B * Lq, Hq * D] (bf16, rows of any stride) over the
     first lens[b] positions of each stream's NVFP4 cache into o; scale None:
     1 / sqrt(D)."""
-    import torch
-    dev = torch.cuda.current_device()
-    H, D, pages, page, mp = _kv4(dev, k_q, k_s, v_q, v_s, k_ts, v_ts, table, B)
-    _on(dev, torch.bfloat16, q, o)
-    _on(dev, torch.int32, lens, q_lens)
-    _sized(lens, B, "lens")
-    _sized(q_lens, B, "q_lens")
-    _solid(dev, torch.uint8, ws)
-    _check("attn_kv4", lib().attn_kv4(
-        _ptr(q), _rows(q, B * Lq, Hq * D, "q"), B, Lq, Hq, H, D, _ptr(k_q), _ptr(k_s), _ptr(v_q),
-        _ptr(v_s), _ptr(k_ts), _ptr(v_ts), pages, page, _ptr(table), mp, _ptr(lens),
-        _ptr(q_lens), 1 if causal else 0, D ** -0.5 if scale is None else scale, _ptr(o),
-        _rows(o, B * Lq, Hq * D, "o"), _ptr(ws), _nbytes(ws), _current(stream, dev)))
+    status = _native().attn_kv4(q, k_q, k_s, v_q, v_s, k_ts, v_ts, table, lens, o, B, Lq, Hq, q_lens,
+                                causal, scale, ws, stream)
+    if status:
+        _check("attn_kv4", status)
 
 
 def attn_cross_workspace(B, Lq, Lk, Hq, Hkv, D):
@@ -563,22 +463,9 @@ def attn_cross(q, k, v, o, B, Lq, Lk, Hq, Hkv, D, k_lens=None, mask=None, scale=
     [B * Lk, Hkv * D] (bf16, rows of any stride) into o: the states before
     k_lens[b] (int32) with mask[b][j] != 0 (uint8 or bool [B, Lk]); scale
     None: 1 / sqrt(D)."""
-    import torch
-    dev = torch.cuda.current_device()
-    if mask is not None and mask.dtype == torch.bool:
-        mask = mask.view(torch.uint8)
-    _on(dev, torch.bfloat16, q, k, v, o)
-    _on(dev, torch.int32, k_lens)
-    _solid(dev, torch.uint8, mask, ws)
-    _sized(k_lens, B, "k_lens")
-    if mask is not None and (mask.dim() != 2 or mask.shape[0] < B or mask.shape[1] != Lk):
-        raise ValueError(f"mask: needs shape [{B}, {Lk}], got {tuple(mask.shape)}")
-    w = Hkv * D
-    _check("attn_cross", lib().attn_cross(
-        _ptr(q), _rows(q, B * Lq, Hq * D, "q"), _ptr(k), _rows(k, B * Lk, w, "k"), _ptr(v),
-        _rows(v, B * Lk, w, "v"), B, Lq, Lk, Hq, Hkv, D, _ptr(k_lens), _ptr(mask),
-        D ** -0.5 if scale is None else scale, _ptr(o), _rows(o, B * Lq, Hq * D, "o"), _ptr(ws),
-        _nbytes(ws), _current(stream, dev)))
+    status = _native().attn_cross(q, k, v, o, B, Lq, Lk, Hq, Hkv, D, k_lens, mask, scale, ws, stream)
+    if status:
+        _check("attn_cross", status)
 
 
 # ------------------------------------------------------- host decisions --

@@ -1,19 +1,23 @@
-"""Build libqact.so (the HIP kernels and the C ABI) for gfx950 with hipcc.
+"""Build libqact.so (the HIP kernels and the C ABI) for gfx950 with hipcc, and
+_call.so (the compiled Python calls) with the host compiler.
 
 Run as ``python -m mixed_precision_quantized_act_amd.build`` or through
 ``__graft_entry__.build()``.  Each source compiles to its own object in
 parallel (the GEMM sources hold many kernel instantiations), then one link
 writes the library next to this file.
 """
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqact.so")
+CALL = os.path.join(HERE, "_call.so")
 ROOT = os.path.dirname(HERE)
 OBJ_DIR = os.path.join(HERE, "_build")
 
@@ -42,7 +46,22 @@ def _run(cmd):
     r = subprocess.run(cmd, capture_output=True, text=True)
     err = "\n".join(l for l in r.stderr.splitlines() if "packed-fp32-ops" not in l)
     if r.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + " ".join(cmd) + "\n" + err)
+        raise RuntimeError("compiler failed:\n" + " ".join(cmd) + "\n" + err)
+
+
+def call_command(out):
+    """The compiler's line for _call.so (it finds PyTorch's libraries loaded)."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no host C++ compiler found")
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+    include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]
+    return ([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
+             "-I", os.path.join(ROOT, "include")] + [x for d in include for x in ("-isystem", d)]
+            + [os.path.join(CSRC, "pycall.cpp"), "-o", out, "-L", os.path.join(torch, "lib"),
+               "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"])
 
 
 def build(verbose=True):
@@ -52,12 +71,15 @@ def build(verbose=True):
     for src in SOURCES:
         obj = os.path.join(OBJ_DIR, os.path.splitext(src)[0] + ".o")
         jobs.append(([cc] + FLAGS + ["-c", os.path.join(CSRC, src), "-o", obj], obj))
+    call = call_command(CALL + ".tmp")
+    commands = [call] + [cmd for cmd, _ in jobs]
     if verbose:
-        for cmd, _ in jobs:
+        for cmd in commands:
             print(" ".join(cmd), flush=True)
-    workers = max(1, min(len(jobs), os.cpu_count() or 1))
+    workers = max(1, min(len(commands), os.cpu_count() or 1))
     with ThreadPoolExecutor(max_workers=workers) as ex:
-        list(ex.map(_run, [cmd for cmd, _ in jobs]))
+        list(ex.map(_run, commands))
+    os.replace(CALL + ".tmp", CALL)
     tmp = LIB + ".tmp"
     link = [cc, "--offload-arch=gfx950", "-shared", "-fPIC"] + [o for _, o in jobs] + ["-o", tmp]
     if verbose:
