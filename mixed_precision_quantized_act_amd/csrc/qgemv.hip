@@ -26,8 +26,8 @@
 // elements at a time: a line of codes.  More weight rows read the activations
 // less often (32 rows of 8192 against 16384 weight rows: 83, 51 and 35 us;
 // 1 row: 26.7, 22.5 and 20.8 us) but leave fewer workgroups (16 rows of 7680
-// against 1920: 12.8, 15.8 and 23.8 us): as many as leave each of the 256
-// compute units one.
+// against 1920: 12.8, 15.8 and 23.8 us) or full rounds of them (2 rows of 4096
+// against 12288: 14.8, 14.5 and 13.2 us, against 24576: 23.4, 19.6 and 24.4).
 //
 // Against few weight rows the activations are what a compute unit reads most
 // of, so their rows are then shared out as well, 8 or 16 to a workgroup (16 rows
@@ -421,8 +421,17 @@ hipError_t launch_qgemv(const uint16_t* x, int64_t ldx, const uint8_t* w_q, cons
                         const float* w_ts, int64_t M, int64_t N, int64_t K, const GemmOut& o,
                         hipStream_t stream) {
   const GemvArgs a = {x, ldx, w_q, w_s, w_ts, (int)M, N, K, o.bias, o.y, o.ldy, o.out_f32, o.gelu};
-  if (N >= kGvPlaces * 4 * kGvRows) return launch<4>(a, stream);
-  if (N >= kGvPlaces * 2 * kGvRows) return launch<2>(a, stream);
+  // The time of the fullest compute unit in tiles of 16 weight rows: the rounds
+  // of workgroups (8 waves a unit) by what a tile costs among 1, 2 or 4.
+  const int64_t nsteps = (K + kGvStep - 1) / kGvStep;
+  const int64_t places = kGvPlaces * kGvWaves / (nsteps < kGvWaves ? nsteps : kGvWaves);
+  const auto load = [&](int64_t rt, double each) {
+    const int64_t groups = (N + kGvRows * rt - 1) / (kGvRows * rt);
+    return (double)((groups + places - 1) / places * rt) * each;
+  };
+  const double one = load(1, M <= 8 ? 1.4 : 1.5), two = load(2, M <= 8 ? 1.05 : 1.1), four = load(4, 1.0);
+  if (four <= two && four <= one) return launch<4>(a, stream);
+  if (two <= one) return launch<2>(a, stream);
   return launch<1>(a, stream);
 }
 

@@ -64,3 +64,13 @@ def test_rows_shared_out_over_workgroups(M, N):
     x, w, b = _case(M, N, 288, 14)
     y, e = _expect(x, w, b, False)
     _close(_call(x, w, N, 288, b, False, ldx=296, ldy=N + 3), y, e, False)
+
+
+@pytest.mark.parametrize("N", [8200, 12290])
+def test_large_weights(N):
+    """Sizes at which a workgroup takes 32 and 64 weight rows, of one weight for all row counts."""
+    K = 2064
+    x, w, b = _case(32, N, K, 15)
+    y, e = _expect(x, w, b, True)
+    for M in (1, 3, 8, 9, 16, 17, 32):
+        _close(_call(x[:M], w, N, K, b, True, gelu=True), y[:M], e[:M], True)
