@@ -11,6 +11,7 @@ namespace {
 
 // How a row tile's keys are cut: n pieces, each `size` parts of `whole` and
 // the last one what is left.
+constexpr int kCuts = 64;
 struct Pieces {
   int n, size, whole;
 };
@@ -319,44 +320,48 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, Pieces pc, Gat
 constexpr int kTileWaves = 8;
 constexpr int kTileRows = 32 * kTileWaves;
 
-// One workgroup fits a CU: this many run at once.  Row tiles that do not fill
-// them (or fill them badly) have their keys cut into pieces: S equal ones, or
-// as many large ones as fit at once and a small one for the places that are
-// left, which takes each of those several times.  The cost in us: the
-// time of the slowest place, and for more than one piece the partial sums,
-// written and read again, and the launch that joins them.
+// One workgroup fits a compute unit: this many run at once.  Row tiles that do
+// not fill them (or fill them badly) have their keys cut into pieces: n equal
+// ones, or n - 1 large ones that all run at once and a small one for the places
+// that are left, which take k of those each.  The cost in us: the time of the
+// slowest place, a workgroup being kTileStart and kTileTime a tile of keys, and for
+// more than one piece the partial sums, written and read again, and the launch
+// that joins them.  (1350 rows, 30 heads of 64, 12376 keys: 180 row tiles, so one
+// piece leaves 76 places idle.  Two pieces, the large one 0.70, 0.75, 0.80 and
+// 0.85 of the keys: 218, 187, 181 and 190 us; 3, 4 and 7 equal ones: 237, 190 and
+// 203.)
 constexpr int64_t kPlaces = 256;
+constexpr double kTileStart = 8.0;
+template <int D>
+constexpr double kTileTime = D == 64 ? 0.97 : 1.7;
 
 Pieces pieces_of(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L, size_t ws_bytes) {
   const int64_t rows = B * Lq * Hq;
   const int64_t u = B * Hkv * ((Lq * (Hq / Hkv) + kTileRows - 1) / kTileRows);
   const int64_t chunks = (L + kTileKeys - 1) / kTileKeys;
-  const double tau = D == 64 ? 1.1 : 1.9;                      // us a tile of keys
+  const double T = (double)chunks * (D == 64 ? kTileTime<64> : kTileTime<128>);
   const int64_t fit = (int64_t)(ws_bytes / AttnSplit::bytes(rows, D));
   Pieces best = {1, 1, 1};
   double least = 0.0;
   for (int n = 1; n <= 16; ++n) {
     if (n > 1 && (n > fit || n > chunks)) break;
-    for (int uneven = 0; uneven < 2; ++uneven) {
-      Pieces p = {n, 1, n};
-      double span;                                              // of the slowest place, of `whole`
-      if (!uneven) {
-        const int64_t k = u * n;
-        span = (double)((k + kPlaces - 1) / kPlaces);
-      } else {
-        const int64_t left = kPlaces - u * (n - 1);             // places beside the large pieces
-        if (n < 2 || left <= 0) continue;
-        p.size = (int)((u + left - 1) / left);
-        if (p.size < 2) continue;
-        p.whole = (n - 1) * p.size + 1;
-        span = p.size;
-      }
-      double cost = span / p.whole * (double)chunks * tau;
-      if (n > 1) cost += 4.0 + (double)n * (double)rows * D * 4 * 1.5 / 4e6;
-      if (n == 1 || cost < least) {
-        least = cost;
-        best = p;
-      }
+    const double joined = n > 1 ? 4.0 + (double)n * (double)rows * D * 4 * 1.5 / 4e6 : 0.0;
+    const double equal = (double)((u * n + kPlaces - 1) / kPlaces) * (T / n + kTileStart) + joined;
+    if (n == 1 || equal < least) {
+      least = equal;
+      best = {n, 1, n};
+    }
+    const int64_t left = kPlaces - u * (n - 1);               // places beside the large pieces
+    if (n < 2 || left <= 0) continue;
+    const double k = (double)((u + left - 1) / left);
+    // the large part f for which both kinds of places take the same time
+    const double f = (k + (k - 1.0) * kTileStart / T) / (1.0 + k * (n - 1));
+    const int size = (int)(f * kCuts + 0.5);
+    if (size * (n - 1) >= kCuts) continue;
+    const double uneven = f * T + kTileStart + joined;
+    if (uneven < least) {
+      least = uneven;
+      best = {n, size, kCuts};
     }
   }
   return best;
