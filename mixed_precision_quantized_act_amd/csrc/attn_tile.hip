@@ -162,7 +162,7 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, Pieces pc, Gat
   const int end = src.causal ? n - (nq - 1 - last / G) : n;
   const int chunks = (max(end, 0) + kTileKeys - 1) / kTileKeys;
   const int c0 = (int)((int64_t)chunks * (piece * pc.size) / pc.whole);
-  const int c1 = (int)((int64_t)chunks * min(piece * pc.size + pc.size, pc.whole) / pc.whole);
+  const int c1 = piece == pc.n - 1 ? chunks : (int)((int64_t)chunks * ((piece + 1) * pc.size) / pc.whole);
   const int base0 = c0 * kTileKeys, nt = c1 - c0;
   // tiles of which this wave's rows see anything
   const int mine = min(nt, max(0, (wend - base0 + kTileKeys - 1) / kTileKeys));
