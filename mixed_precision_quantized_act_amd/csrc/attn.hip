@@ -10,7 +10,9 @@ namespace qact {
 
 namespace {
 
-// Rows of a key head from which the tiles of many rows are used.
+// Rows of a key head from which the tiles of many rows are used (4 streams of 8
+// key heads of 128, 4000 tokens: 64 rows 22.8 us, by the few rows' kernel 27.7;
+// one stream of 8 heads of 64, 8000 tokens: 48 rows 17.3 and 14.2).
 constexpr int64_t kManyRows = 64;
 
 bool many(int64_t Lq, int Hq, int Hkv) { return Lq * (Hq / Hkv) >= kManyRows; }
