@@ -14,6 +14,10 @@
 // NVFP4 (9/16 byte per element): one conversion (half rate) and one packed
 // multiply per two elements, about 0.6 of the VALU's time at 5 TB/s; sixteen
 // rows cost no more than one.
+//
+// 16 streams of 16384 to 32768 tokens, one query token each, 32 query and 8 key
+// heads of 128: 100 us and 4.6 for the join, 463 MB at 4.4 TB/s.  24 tokens to 300 to
+// 1500 bf16 states, 20 heads of 64: 27 us and 4.4.
 #include "attn_common.h"
 
 namespace qact {

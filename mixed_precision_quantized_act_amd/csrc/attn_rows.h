@@ -21,7 +21,9 @@
 namespace qact {
 
 constexpr int kTileKeys = 64;
-// A weight is p 2^kTileBias relative to the reference, which moves when the
+// A weight is rounded once, to the operand's type (2^-11 or 2^-8 relative: no
+// MFMA takes more), and the sums are of rounded weights.  It is p 2^kTileBias
+// relative to the reference, which moves when the
 // weights of 32 keys sum to more than kTileMost (2^8 times a weight of 1).
 template <bool F16>
 constexpr float kTileBias = F16 ? 7.0f : 0.0f;
@@ -110,7 +112,7 @@ struct Rows {
         const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i], c, shift));
         const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i + 1], c, shift));
         p[i >> 2][i & 3] = pack16<F16>(e0, e1);
-        sum += e0 + e1;
+        sum = add_pair<F16>(p[i >> 2][i & 3], sum);
       }
       sum = pair_sum(sum);
     }
@@ -242,7 +244,9 @@ __device__ __forceinline__ void hide(f32x16& s, uint32_t seen) {
 template <bool F16, int D>
 __device__ __forceinline__ void store_rows(const Rows<F16, D>& r, float v_scale, uint16_t* dst, int h,
                                            bool on) {
-  const float f = r.l == 0.0f ? 0.0f : v_scale / r.l;
+  // (one last place of float32, before the rounding to bf16; a row's largest
+  // weight is near its reference's 1, so the sum is a normal number)
+  const float f = r.l == 0.0f ? 0.0f : v_scale * __builtin_amdgcn_rcpf(r.l);
 #pragma unroll
   for (int d = 0; d < D / 32; ++d)
 #pragma unroll

@@ -3,6 +3,12 @@
 // 64 that it stages in shared memory as 16-bit operands (an NVFP4 tile is
 // expanded once for all rows), ahead of what its MFMAs read.  attn_rows.h says
 // what a wave does with them and what bounds it.
+//
+// 1350 rows to 12376 tokens of a cache, 30 heads of 64: 179 us with the join, 128
+// GFLOP at 0.72 PFLOP/s (a large library product: 1.21); heads of 128, 16 of
+// them: 157 us.  Counters: VALU busy 0.42 of the cycles, MFMA 0.31, both waves of
+// a SIMD waiting for data or each other a third of the time.  Why 8 waves: with 4
+// a tile is staged for half as many rows (195 us; 3 of them per SIMD spill, 190).
 #include "attn_rows.h"
 
 namespace qact {
