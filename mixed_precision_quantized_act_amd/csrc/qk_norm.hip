@@ -15,7 +15,7 @@
 // of ONE token, so that the token's table row and the norm's weights are read
 // once per wave and not once per head.
 //
-// 17776 tokens, 30 + 30 heads of 64, layer norm, pairs: 60 us, 273 MB at 4.5
+// 17776 tokens, 30 + 30 heads of 64, layer norm, pairs: 55.5 us, 273 MB at 4.9
 // TB/s (a copy reaches 5.1).  What is left to do per element is the VALU's
 // work; exchanges through shared memory, weights of both kinds per wave, and
 // a division of 64 bits took it from 60 to 78 us.
@@ -26,8 +26,11 @@ namespace qact {
 
 namespace {
 
-// heads of a token taken one after the other by a lane group (2: 65 us, 8: 75)
+// Heads of a token taken one after the other by a lane group (17776 tokens: 2
+// 58 us, 4 55.5, 6 59); of few tokens one, so that more waves share them (9 tokens,
+// 32 + 8 heads of 128: 4 4.8 us, 1 3.9).
 constexpr int kQkHeads = 4;
+constexpr int64_t kQkWaves = 2048;
 
 __device__ __forceinline__ void unpack8(u32x4 w, float (&f)[8]) {
 #pragma unroll
@@ -158,20 +161,28 @@ qk_norm_rope_kernel(QkArgs a, int qchunks, int chunks, Gate gate) {
       }
     }
     if (in && h < H)
-      *reinterpret_cast<u32x4*>(dst + (int64_t)h * D + 8 * l) =
-          u32x4{bf16_pack(x[0], x[1]), bf16_pack(x[2], x[3]), bf16_pack(x[4], x[5]),
-                bf16_pack(x[6], x[7])};
+      // (past the caches: left dirty there, the last of them would be written back
+      // after the kernel; 60 and 55.5 us)
+      __builtin_nontemporal_store(u32x4{bf16_pack(x[0], x[1]), bf16_pack(x[2], x[3]),
+                                        bf16_pack(x[4], x[5]), bf16_pack(x[6], x[7])},
+                                  reinterpret_cast<u32x4*>(dst + (int64_t)h * D + 8 * l));
   }
+}
+
+template <int LPH, int U>
+hipError_t launch(const QkArgs& a, hipStream_t stream) {
+  const int per = 64 / LPH * U;
+  const int qchunks = (a.Hq + per - 1) / per, chunks = qchunks + (a.Hk + per - 1) / per;
+  const dim3 grid((unsigned)((a.M * chunks + 3) / 4));
+  hipLaunchKernelGGL((qk_norm_rope_kernel<LPH, U>), grid, dim3(256), 0, stream, a, qchunks, chunks,
+                     current_gate());
+  return hipGetLastError();
 }
 
 template <int LPH>
 hipError_t launch(const QkArgs& a, hipStream_t stream) {
-  const int per = 64 / LPH * kQkHeads;
-  const int qchunks = (a.Hq + per - 1) / per, chunks = qchunks + (a.Hk + per - 1) / per;
-  const dim3 grid((unsigned)((a.M * chunks + 3) / 4));
-  hipLaunchKernelGGL((qk_norm_rope_kernel<LPH, kQkHeads>), grid, dim3(256), 0, stream, a, qchunks,
-                     chunks, current_gate());
-  return hipGetLastError();
+  const int64_t groups = (int64_t)a.M * (a.Hq + a.Hk);              // of lanes, one head each
+  return groups * LPH < kQkWaves * 64 ? launch<LPH, 1>(a, stream) : launch<LPH, kQkHeads>(a, stream);
 }
 
 }  // namespace
