@@ -16,7 +16,7 @@
 // rows cost no more than one.
 //
 // 16 streams of 16384 to 32768 tokens, one query token each, 32 query and 8 key
-// heads of 128: 100 us and 4.6 for the join, 463 MB at 4.4 TB/s.  24 tokens to 300 to
+// heads of 128: 97 us and 4.6 for the join, 463 MB at 4.6 TB/s.  24 tokens to 300 to
 // 1500 bf16 states, 20 heads of 64: 27 us and 4.4.
 #include "attn_common.h"
 
@@ -238,8 +238,10 @@ struct Few<CrossSource, D> {
 };
 
 // Workgroup: (stream, key head, row tile, split), the split running fastest.
+// (Two waves per SIMD keep the compiler from spending more registers than help, 105
+// -> 102 us for 16 streams; bf16 of 128 would spill, 54 -> 75 us.)
 template <class Source, int D>
-__global__ void __launch_bounds__(64 * kFewWaves)
+__global__ void __launch_bounds__(64 * kFewWaves, !Source::kF16 && D == 128 ? 1 : 2)
 attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gate gate) {
   if (gated_off(gate)) return;
   using F = Few<Source, D>;
