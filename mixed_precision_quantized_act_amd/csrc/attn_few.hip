@@ -477,8 +477,11 @@ attn_join_kernel(AttnArgs a, Source src, AttnSplit sp, int splits, Gate gate) {
 
 // Workgroups to aim for: a few for each of the 256 compute units, so that
 // streams of different lengths even out (16 streams of up to 32768 tokens, 8
-// heads of 128: 256 143 us, 512 109, 1024 105, 2048 110).
-constexpr int64_t kFewBlocks = 1024;
+// heads of 128: 256 143 us, 512 109, 1024 105, 2048 110).  Of bf16 heads of 128
+// one workgroup runs at a time on a unit, and each round waits for its first
+// keys: one round (16 tokens to 4000 states, 8 heads: 1024 69 us, 512 60, 256 56, 262
+// MB at 4.7 TB/s).
+constexpr int64_t kFewBlocks = 1024, kFewBlocksWide = 256;
 
 int64_t tiles_of(int64_t B, int64_t Lq, int Hq, int Hkv) {
   return B * Hkv * ((Lq * (Hq / Hkv) + kFewRows - 1) / kFewRows);
@@ -488,10 +491,10 @@ int64_t tiles_of(int64_t B, int64_t Lq, int Hq, int Hkv) {
 // 1.8 us of a nearly empty chip and the join 0.22 us a split, so of w steps
 // more than sqrt(8 w) splits cost more than they give (one stream of 32768: 32
 // splits 21 us, 64 25, 128 37).
-int64_t splits_of(int64_t B, int64_t Lq, int Hq, int Hkv, int64_t L) {
+int64_t splits_of(int64_t B, int64_t Lq, int Hq, int Hkv, int64_t L, int64_t blocks) {
   const int64_t tiles = tiles_of(B, Lq, Hq, Hkv);
   const int64_t w = (L + kFewKeys * kFewWaves - 1) / (kFewKeys * kFewWaves);
-  int64_t s = (kFewBlocks + tiles - 1) / tiles;
+  int64_t s = (blocks + tiles - 1) / tiles;
   s = s < w ? s : w;
   while (s > 1 && s * s > 8 * w) --s;
   if (s <= 1) return 1;
@@ -502,7 +505,7 @@ int64_t splits_of(int64_t B, int64_t Lq, int Hq, int Hkv, int64_t L) {
 }  // namespace
 
 size_t attn_few_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
-  const int64_t s = splits_of(B, Lq, Hq, Hkv, L);
+  const int64_t s = splits_of(B, Lq, Hq, Hkv, L, kFewBlocks);    // (a source may take fewer)
   return s > 1 ? s * AttnSplit::bytes(B * Lq * Hq, D) : 0;
 }
 
@@ -510,7 +513,7 @@ template <class Source>
 hipError_t launch_attn_few(const AttnArgs& a, const Source& src, int64_t L, void* ws,
                            size_t ws_bytes, hipStream_t stream) {
   const int64_t rows = a.B * a.Lq * a.Hq;
-  int64_t s = splits_of(a.B, a.Lq, a.Hq, a.Hkv, L);
+  int64_t s = splits_of(a.B, a.Lq, a.Hq, a.Hkv, L, !Source::kF16 && a.D == 128 ? kFewBlocksWide : kFewBlocks);
   const int64_t fit = (int64_t)(ws_bytes / AttnSplit::bytes(rows, a.D));
   if (s > fit) s = fit > 1 ? fit : 1;
   const AttnSplit sp = AttnSplit::in(ws, s, rows, a.D);
