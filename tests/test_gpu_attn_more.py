@@ -287,3 +287,10 @@ def test_cross_more_of_few_states(Lk, Lq, Hq, H):
     m[0, 130:] = False
     _cross(29, 2, Lq, Lk, Hq, H, 64)
     _cross(29, 2, Lq, Lk, Hq, H, 64, mask=m, k_lens=[Lk, Lk - 100])
+
+
+@pytest.mark.parametrize("Lq", [1, 5])
+@pytest.mark.parametrize("D", [64, 128])
+def test_kv4_short_streams_behind_a_large_table(Lq, D):
+    """Streams of 5 to 3000 tokens of a table for 100000: each takes the splits that its own length is worth."""
+    _kv4(33, 4, Lq, 4, 2, D, 64, [5, 3000, 257, 700], extra_pages=1500, bad=[(0, 3, -1)])
