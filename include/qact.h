@@ -481,7 +481,9 @@ int qk_norm_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int6
  *   D 64 or 128; Hq a multiple of H; scale > 0; B Lq Hq < 2^24.
  *   ws: with attn_kv4_workspace() bytes a call with few query rows splits
  *   the keys over more workgroups; less (also none) splits less.  The sums
- *   are made in an order that the sizes and ws_bytes decide.  Calls (and
+ *   are made in an order that the sizes and ws_bytes decide.  The work is laid
+ *   out for max_pages: a table much longer than its streams costs short ones up
+ *   to twice their time.  Calls (and
  *   replayed graphs) that may run at the same time need workspaces of their
  *   own; calls in order on one stream may share one.
  * ------------------------------------------------------------------------ */

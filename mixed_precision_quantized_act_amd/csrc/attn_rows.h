@@ -215,6 +215,18 @@ struct Rows {
       o[i % (D / 32)] = mfma32<F16>(v_operand<VO>(v, va, i / (D / 32), i % (D / 32)),
                                     p[i / (D / 32)], o[i % (D / 32)]);
   }
+  // f o as bf16, elements 32 d + 2 i + 8 h .. + 7 of the lane's row (i: 0 or 8):
+  // it holds 8 (i / 4) + 4 h + 0..3 and 8 (i / 4 + 1) + 4 h + 0..3 of them, lanes
+  // l and l + 32 exchange halves.
+  __device__ __forceinline__ u32x4 out8(int d, int i, float f) const {
+    const auto w0 = __builtin_amdgcn_permlane32_swap(bf16_pack(o[d][i] * f, o[d][i + 1] * f),
+                                                     bf16_pack(o[d][i + 4] * f, o[d][i + 5] * f),
+                                                     false, false);
+    const auto w1 = __builtin_amdgcn_permlane32_swap(bf16_pack(o[d][i + 2] * f, o[d][i + 3] * f),
+                                                     bf16_pack(o[d][i + 6] * f, o[d][i + 7] * f),
+                                                     false, false);
+    return {w0[0], w1[0], w0[1], w1[1]};
+  }
 };
 
 // What is not seen of 32 keys: minus infinity.  `seen` from the first of
@@ -251,16 +263,8 @@ __device__ __forceinline__ void store_rows(const Rows<F16, D>& r, float v_scale,
   for (int d = 0; d < D / 32; ++d)
 #pragma unroll
     for (int i = 0; i < 16; i += 8) {
-      // elements 8 (i / 4) + 4 h + 0..3 and 8 (i / 4 + 1) + 4 h + 0..3: lanes l and
-      // l + 32 exchange halves, so that each holds 8 consecutive ones
-      const auto w0 = __builtin_amdgcn_permlane32_swap(
-          bf16_pack(r.o[d][i] * f, r.o[d][i + 1] * f),
-          bf16_pack(r.o[d][i + 4] * f, r.o[d][i + 5] * f), false, false);
-      const auto w1 = __builtin_amdgcn_permlane32_swap(
-          bf16_pack(r.o[d][i + 2] * f, r.o[d][i + 3] * f),
-          bf16_pack(r.o[d][i + 6] * f, r.o[d][i + 7] * f), false, false);
-      if (on)
-        *reinterpret_cast<u32x4*>(dst + 32 * d + 2 * i + 8 * h) = u32x4{w0[0], w1[0], w0[1], w1[1]};
+      const u32x4 w = r.out8(d, i, f);
+      if (on) *reinterpret_cast<u32x4*>(dst + 32 * d + 2 * i + 8 * h) = w;
     }
 }
 

@@ -4,12 +4,12 @@
 // rows, 32 at a time, without meeting again; the next 32 are on their way
 // meanwhile.  attn_rows.h says what a wave does with them.
 //
-// 30 heads of 64, 17550 query tokens, 226 states: 61 us, 0.50 us of a SIMD for
+// 30 heads of 64, 17550 query tokens, 226 states: 56 us, 0.50 us of a SIMD for
 // 32 rows by 64 keys (the alternating products and weights alone take 0.41 us
-// of it) and 27 us for the rest: launch, staging, each block's first and last
-// products and its rows' load and store.  A memory that is read and written
-// once would take 27 us.  Stored as whole lines through shared memory, the rows
-// cost 1 us less; 12 waves instead of 8 spill registers and cost 6 us more.
+// of it) and about 20 us for the rest: launch, staging, each block's first and
+// last products and its rows' load and store.  A memory that is read and written
+// once would take 27 us.  12 waves instead of 8 spill registers and cost 6 us
+// more.
 #include "attn_rows.h"
 
 namespace qact {
@@ -34,7 +34,9 @@ attn_short_kernel(AttnArgs a, CrossSource src, int blocks, int shares, Gate gate
   constexpr int kBytes = kTileKeys * D * 2, kHalf = kBytes / 2, kPieces = D / 8;
   // K, V, and half a tile of zeros: the values before the first tile
   constexpr int kZeros = kTiles * kBytes - kHalf;              // (read from + kHalf on)
-  __shared__ __align__(16) char lds[2 * kTiles * kBytes + kHalf];
+  constexpr bool kLines = D == 64 && kTiles == 4;
+  constexpr int kOut = 2 * kTiles * kBytes + kHalf;
+  __shared__ __align__(16) char lds[kOut + (kLines ? W * 32 * 2 * D : 0)];
   char* const kt = lds;
   char* const vt = lds + kTiles * kBytes;
 
@@ -57,6 +59,36 @@ attn_short_kernel(AttnArgs a, CrossSource src, int blocks, int shares, Gate gate
     for (int i = 0; i < D / 16; ++i) next[i] = *reinterpret_cast<const u32x4*>(p + 16 * i);
   };
   if (block < last) fetch(block);
+  // Finished rows: where the shared memory has room for them, through it, so that
+  // a store writes whole lines, past the caches, whose last dirty lines would be
+  // written back after the kernel (60 -> 56 us; whole lines alone: 61).
+  R r;
+  auto store = [&](int block) {
+    if constexpr (kLines) {
+      char* const out = lds + kOut + wave * (32 * 2 * D);
+      const float f = r.l == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(r.l);
+      wave_lds_order();
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 8)
+          *reinterpret_cast<u32x4*>(out + k_piece<D>(col, 4 * d + i / 4 + h)) = r.out8(d, i, f);
+      wave_lds_order();
+#pragma unroll
+      for (int j = 0; j < kPieces / 2; ++j) {
+        const int line = j * (64 / kPieces) + lane / kPieces, c = lane % kPieces;
+        const int row = 32 * block + line, t = G == 1 ? row : row / G;
+        const u32x4 w = *reinterpret_cast<const u32x4*>(out + k_piece<D>(line, c));
+        if (row < rows)
+          __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(
+              a.o + (b * a.Lq + t) * a.ldo + (int64_t)(hk * G + row - t * G) * D + 8 * c));
+      }
+    } else {
+      const int row = 32 * block + col, t = G == 1 ? row : row / G;
+      store_rows(r, 1.0f, a.o + (b * a.Lq + t) * a.ldo + (int64_t)(hk * G + row - t * G) * D, h,
+                 row < rows);
+    }
+  };
   // a thread's pieces of the keys; what is not seen may hold NaN and is zeroed
   // when that is known
   constexpr int kLoads = kTiles * kTileKeys * kPieces / (64 * W);
@@ -92,7 +124,6 @@ attn_short_kernel(AttnArgs a, CrossSource src, int blocks, int shares, Gate gate
 #pragma unroll
   for (int d = 0; d < D / 32; ++d)
     va[d] = kZeros + v_piece<D>(4 * h + ((lane & 15) >> 2), 4 * d + 2 * ((lane >> 4) & 1)) + 8 * (lane & 3);
-  R r;
   r.set_ones(lane);
   r.c = fmaxf(a.scale * kLog2e, 0x1p-126f);
   for (; block < last; block += W) {
@@ -128,9 +159,7 @@ attn_short_kernel(AttnArgs a, CrossSource src, int blocks, int shares, Gate gate
     // wait for the next rows here, not behind the stores of these
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) asm volatile("" : "+v"(next[i]));
-    const int row = 32 * block + col, t = G == 1 ? row : row / G;
-    store_rows(r, 1.0f, a.o + (b * a.Lq + t) * a.ldo + (int64_t)(hk * G + row - t * G) * D, h,
-               row < rows);
+    store(block);
   }
 }
 
