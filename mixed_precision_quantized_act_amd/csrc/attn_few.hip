@@ -16,7 +16,7 @@
 // rows cost no more than one.
 //
 // 16 streams of 16384 to 32768 tokens, one query token each, 32 query and 8 key
-// heads of 128: 97 us and 4.6 for the join, 463 MB at 4.6 TB/s.  24 tokens to 300 to
+// heads of 128: 90 us and 4.6 for the join, 463 MB at 5.1 TB/s.  24 tokens to 300 to
 // 1500 bf16 states, 20 heads of 64: 27 us and 4.4.
 #include "attn_common.h"
 
@@ -31,14 +31,23 @@ constexpr int kFewWaves = 4;
 typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-template <class Source, int D>
+// Once: no other workgroup reads the same keys (one tile of rows), so they go past
+// the caches (16 streams of up to 32768 tokens: 101 -> 94 us; read by two tiles of
+// rows, 109 -> 116, and bf16 states, whose lines take two loads, 30 -> 33).
+template <bool Once, class T>
+__device__ __forceinline__ T fetch(const void* p) {
+  if constexpr (Once) return __builtin_nontemporal_load(static_cast<const T*>(p));
+  return *static_cast<const T*>(p);
+}
+
+template <class Source, int D, bool Once>
 struct Few;
 
 // NVFP4: per 64 keys a lane holds for each of four 16-key tiles the codes of
 // D/4 elements of key (lane & 15) and their group scales, V's codes as they lie
 // and the group scales of V's key `lane`.
-template <int D>
-struct Few<Kv4Source, D> {
+template <int D, bool Once>
+struct Few<Kv4Source, D, Once> {
   static constexpr int kKWords = D / 32;              // code words per lane and tile
   static constexpr int kVLoads = kFewKeys * D / 2 / 16 / 64;
   static constexpr int kGroups = D / 16;
@@ -70,12 +79,12 @@ struct Few<Kv4Source, D> {
       const uint8_t* kq = s.c.k_q + slot[t] * (D / 2) + (key * (D / 2) + 4 * kKWords * g);
       const uint8_t* ks = s.c.k_s + slot[t] * kGroups + (key * kGroups + kKWords / 2 * g);
       if constexpr (D == 128) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(kq);
+        const u32x4 w = fetch<Once, u32x4>(kq);
 #pragma unroll
         for (int i = 0; i < 4; ++i) r.k[t][i] = w[i];
         r.ks[t] = *reinterpret_cast<const uint16_t*>(ks);
       } else {
-        const u32x2 w = *reinterpret_cast<const u32x2*>(kq);
+        const u32x2 w = fetch<Once, u32x2>(kq);
         r.k[t][0] = w[0];
         r.k[t][1] = w[1];
         r.ks[t] = *ks;
@@ -89,7 +98,7 @@ struct Few<Kv4Source, D> {
       const int64_t lo = slot[(D == 128 ? u : 2 * u) % 4], hi = slot[(D == 128 ? u : 2 * u + 1) % 4];
       const int64_t at = lane < 32 ? lo : hi;
       if (at >= 0)
-        r.v[u] = *reinterpret_cast<const u32x4*>(s.c.v_q + (at + (vk & 15)) * (D / 2) + 16 * (x % (D / 32)));
+        r.v[u] = fetch<Once, u32x4>(s.c.v_q + (at + (vk & 15)) * (D / 2) + 16 * (x % (D / 32)));
     }
 #pragma unroll
     for (int i = 0; i < (kGroups + 3) / 4; ++i) r.vs[i] = 0;
@@ -173,7 +182,7 @@ struct Few<Kv4Source, D> {
 
 // bf16 states.
 template <int D>
-struct Few<CrossSource, D> {
+struct Few<CrossSource, D, false> {
   static constexpr int kK = D / 32;                    // 16-byte pieces per lane and tile
   static constexpr int kVLoads = kFewKeys * D * 2 / 16 / 64;
   static constexpr int kLds = kFewKeys * D * 2;
@@ -240,11 +249,11 @@ struct Few<CrossSource, D> {
 // Workgroup: (stream, key head, row tile, split), the split running fastest.
 // (Two waves per SIMD keep the compiler from spending more registers than help, 105
 // -> 102 us for 16 streams; bf16 of 128 would spill, 54 -> 75 us.)
-template <class Source, int D>
+template <class Source, int D, bool Once>
 __global__ void __launch_bounds__(64 * kFewWaves, !Source::kF16 && D == 128 ? 1 : 2)
 attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gate gate) {
   if (gated_off(gate)) return;
-  using F = Few<Source, D>;
+  using F = Few<Source, D, Once>;
   constexpr bool kF16 = Source::kF16;
   constexpr int kJoin = kFewWaves * kFewRows * (D + 4) * 4;       // the waves' sums
   constexpr int kLds = kFewWaves * F::kLds > kJoin ? kFewWaves * F::kLds : kJoin;
@@ -518,14 +527,19 @@ hipError_t launch_attn_few(const AttnArgs& a, const Source& src, int64_t L, void
   if (s > fit) s = fit > 1 ? fit : 1;
   const AttnSplit sp = AttnSplit::in(ws, s, rows, a.D);
   const int64_t tiles = (a.Lq * (a.Hq / a.Hkv) + kFewRows - 1) / kFewRows;
+  const dim3 grid((unsigned)(a.B * a.Hkv * tiles * s)), block(64 * kFewWaves);
   const Gate gt = current_gate();
-  const dim3 grid((unsigned)(a.B * a.Hkv * tiles * s));
-  if (a.D == 64)
-    hipLaunchKernelGGL((attn_few_kernel<Source, 64>), grid, dim3(64 * kFewWaves), 0, stream, a,
-                       src, sp, (int)tiles, (int)s, gt);
-  else
-    hipLaunchKernelGGL((attn_few_kernel<Source, 128>), grid, dim3(64 * kFewWaves), 0, stream, a,
-                       src, sp, (int)tiles, (int)s, gt);
+  const auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, src, sp, (int)tiles, (int)s, gt);
+  };
+  if constexpr (Source::kF16) {
+    if (tiles == 1)
+      a.D == 64 ? go(attn_few_kernel<Source, 64, true>) : go(attn_few_kernel<Source, 128, true>);
+    else
+      a.D == 64 ? go(attn_few_kernel<Source, 64, false>) : go(attn_few_kernel<Source, 128, false>);
+  } else {
+    a.D == 64 ? go(attn_few_kernel<Source, 64, false>) : go(attn_few_kernel<Source, 128, false>);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || s == 1) return e;
   return launch_attn_join(a, src, sp, (int)s, stream);
