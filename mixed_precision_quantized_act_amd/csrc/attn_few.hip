@@ -17,7 +17,7 @@
 //
 // 16 streams of 16384 to 32768 tokens, one query token each, 32 query and 8 key
 // heads of 128: 90 us and 4.6 for the join, 463 MB at 5.1 TB/s.  24 tokens to 300 to
-// 1500 bf16 states, 20 heads of 64: 27 us and 4.4.
+// 1500 bf16 states, 20 heads of 64: 24 us and 4.4.
 #include "attn_common.h"
 
 namespace qact {
@@ -33,7 +33,8 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // Once: no other workgroup reads the same keys (one tile of rows), so they go past
 // the caches (16 streams of up to 32768 tokens: 101 -> 94 us; read by two tiles of
-// rows, 109 -> 116, and bf16 states, whose lines take two loads, 30 -> 33).
+// rows: 109 -> 116).  Of bf16 states only the values: a key's line takes two loads
+// (24 tokens to 1500 states: values 30 -> 27 us, both 33).
 template <bool Once, class T>
 __device__ __forceinline__ T fetch(const void* p) {
   if constexpr (Once) return __builtin_nontemporal_load(static_cast<const T*>(p));
@@ -181,8 +182,8 @@ struct Few<Kv4Source, D, Once> {
 };
 
 // bf16 states.
-template <int D>
-struct Few<CrossSource, D, false> {
+template <int D, bool Once>
+struct Few<CrossSource, D, Once> {
   static constexpr int kK = D / 32;                    // 16-byte pieces per lane and tile
   static constexpr int kVLoads = kFewKeys * D * 2 / 16 / 64;
   static constexpr int kLds = kFewKeys * D * 2;
@@ -211,7 +212,7 @@ struct Few<CrossSource, D, false> {
       const int x = u * 64 + lane, vk = x / (D / 8);
       r.v[u] = u32x4{0, 0, 0, 0};
       if (base + vk < n)
-        r.v[u] = *reinterpret_cast<const u32x4*>(s.v + (row0 + vk) * s.ldv + hk * D + 8 * (x % (D / 8)));
+        r.v[u] = fetch<Once, u32x4>(s.v + (row0 + vk) * s.ldv + hk * D + 8 * (x % (D / 8)));
     }
   }
   static __device__ __forceinline__ int q_at(int i, int g) { return 32 * i + 8 * g; }
@@ -532,14 +533,10 @@ hipError_t launch_attn_few(const AttnArgs& a, const Source& src, int64_t L, void
   const auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, src, sp, (int)tiles, (int)s, gt);
   };
-  if constexpr (Source::kF16) {
-    if (tiles == 1)
-      a.D == 64 ? go(attn_few_kernel<Source, 64, true>) : go(attn_few_kernel<Source, 128, true>);
-    else
-      a.D == 64 ? go(attn_few_kernel<Source, 64, false>) : go(attn_few_kernel<Source, 128, false>);
-  } else {
+  if (tiles == 1)
+    a.D == 64 ? go(attn_few_kernel<Source, 64, true>) : go(attn_few_kernel<Source, 128, true>);
+  else
     a.D == 64 ? go(attn_few_kernel<Source, 64, false>) : go(attn_few_kernel<Source, 128, false>);
-  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || s == 1) return e;
   return launch_attn_join(a, src, sp, (int)s, stream);
