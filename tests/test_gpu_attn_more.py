@@ -294,3 +294,32 @@ def test_cross_more_of_few_states(Lk, Lq, Hq, H):
 def test_kv4_short_streams_behind_a_large_table(Lq, D):
     """Streams of 5 to 3000 tokens of a table for 100000: each takes the splits that its own length is worth."""
     _kv4(33, 4, Lq, 4, 2, D, 64, [5, 3000, 257, 700], extra_pages=1500, bad=[(0, 3, -1)])
+
+
+@pytest.mark.parametrize("Lq", [2, 70, 300])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_kv4_a_query_that_is_not_finite_stays_alone(Lq, bad):
+    """Other rows keep finite results near those without it (as above; |v| <= 6 x 448 x 6 / 2688 at most,
+    fp16 weights: 2 x 2^-11 of it, 2^-8 for the outputs' own rounding, each side)."""
+    qa, t = _qa(), torch()
+    case = CacheCase(34, 1, 2, 64, 16, [900])
+    parts = case.device(dev)
+    lens = dev(np.array([900], np.int32))
+    g = t.Generator(device="cuda").manual_seed(12)
+    q = t.randn((Lq, 128), generator=g, device="cuda").bfloat16()
+    o, o2 = t.empty_like(q), t.empty_like(q)
+    ws = _ws(qa.attn_kv4_workspace(1, Lq, 2, 2, 64, case.cache.table.shape[1] * 16))
+    qa.attn_kv4(q, *parts, lens, o, 1, Lq, 2, causal=False, ws=ws)
+    q[1, 9] = bad
+    qa.attn_kv4(q, *parts, lens, o2, 1, Lq, 2, causal=False, ws=ws)
+    assert not o2[1, 64:].isnan().any() and not o2[1, :64].isfinite().all()
+    keep = [i for i in range(Lq) if i != 1]
+    assert float((o2[keep].float() - o[keep].float()).abs().max()) <= 6 * (4 * 2.0 ** -11 + 2 * 2.0 ** -8)
+    assert t.equal(o2[1, 64:], o[1, 64:]) or Lq > 2
+
+
+@pytest.mark.parametrize("Lq,lens", [(1, [3000, 20]), (100, [3000, 150]), (300, [5000, 300])])
+def test_kv4_the_same_bits_every_time(Lq, lens):
+    a = _kv4(35, 2, Lq, 2, 1, 64, 64, lens)
+    for _ in range(3):
+        assert np.array_equal(a, _kv4(35, 2, Lq, 2, 1, 64, 64, lens))
