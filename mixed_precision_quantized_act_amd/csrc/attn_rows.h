@@ -1,12 +1,14 @@
 // Many query rows: what a wave does with 32 of them over tiles of 64 staged
 // keys.
 //
-// What bounds it is the VALU: for heads of 64 the weights of 32 keys take about
-// 165 ns of a SIMD, the two products' MFMAs 121.  Both run at once only when ONE
-// wave's instructions alternate between them (an MFMA and up to 7 VALU
-// instructions: the time of the longer; the same from two waves: nearly the
-// sum), so a wave forms the weights of 32 keys while its MFMAs compute the
-// logits of the next 32 and the second product of the 32 before.
+// VALU and MFMA bound it alike: for heads of 64 the weights of 32 keys take about
+// 118 ns of a SIMD (16 exp2 at 4.4, 24 other instructions at 2.0), the two
+// products' MFMAs and the sums' 123.  Both run at once only when ONE wave's
+// instructions alternate between them (an MFMA and up to 7 VALU instructions: the
+// time of the longer; the same from two waves: nearly the sum), so a wave forms
+// the weights of 32 keys while its MFMAs compute the logits of the next 32 and the
+// second product of the 32 before.  Alternating so, with operands read from shared
+// memory, a step takes 206 ns of a SIMD that two waves share.
 //
 // For the same reason the VALU is left with as little else as possible: no
 // maximum is taken of most tiles.  The weights are formed to the reference that
