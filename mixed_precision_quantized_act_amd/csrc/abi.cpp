@@ -776,11 +776,8 @@ static int check_kv4(const Kv4Cache& c, int64_t B, int page) {
   return QA_OK;
 }
 
-static int log2_of(int page) {
-  int n = 0;
-  while ((1 << n) < page) ++n;
-  return n;
-}
+// (of any `page`: check_kv4 refuses what is not a power of two in its range)
+static int log2_of(int page) { return page > 0 ? 31 - __builtin_clz((unsigned)page) : 0; }
 
 // the four cache arrays and their sizes
 struct Kv4Parts {
