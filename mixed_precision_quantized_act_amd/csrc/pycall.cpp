@@ -65,6 +65,8 @@ struct Place {
   }
 };
 
+// kWhole: what is read as flat memory.  kUnitStep: rows, whose stride the call
+// passes on, and single numbers.
 enum Shape { kUnitStep, kWhole };
 
 // The tensor of an argument, nullptr for None; of this type (bfloat16 also as
@@ -81,7 +83,7 @@ const Tensor* tensor(const Place& p, PyObject* o, const char* name, at::ScalarTy
   if (!t.is_cuda() || t.get_device() != p.dev)
     refuse("%s is on %s, the current device is cuda:%d", name, t.device().str().c_str(), p.dev);
   if (!t.is_contiguous()) {
-    if (shape == kWhole) refuse("%s: a cache, table, weight or mask must be contiguous", name);
+    if (shape == kWhole) refuse("%s: a cache, table, weight, vector or mask must be contiguous", name);
     if (t.size(-1) > 1 && t.stride(-1) != 1) refuse("%s: the last dimension must be contiguous", name);
   }
   return &t;
@@ -189,7 +191,7 @@ PyObject* py_qlinear_bf16(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor* ws = tensor(p, a[2], "w_s", at::kByte, kWhole);
     const Tensor* ts = tensor(p, a[3], "w_ts", at::kFloat);
     const Tensor& y = needed(tensor(p, a[4], "y", out == QA_OUT_F32 ? at::kFloat : at::kBFloat16), "y");
-    const Tensor* bias = tensor(p, a[8], "bias", at::kBFloat16);
+    const Tensor* bias = tensor(p, a[8], "bias", at::kBFloat16, kWhole);
     if (N > 0 && K > 0 && N < (int64_t)1 << 40 && K < (int64_t)1 << 23) {
       sized(wq, N * K / 2, "w_q");
       sized(ws, N * K / 16, "w_s");
@@ -219,7 +221,7 @@ PyObject* py_qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     for (int i = 0; i < 4; ++i) {
       t[i] = tensor(p, a[i], kNames[i], at::kBFloat16);
       if (t[i]) ld[i] = rows(*t[i], M, (int64_t)H[i & 1] * D, kNames[i]);
-      w[i] = tensor(p, a[9 + i], kNorms[i], at::kBFloat16);
+      w[i] = tensor(p, a[9 + i], kNorms[i], at::kBFloat16, kWhole);
       sized(w[i], D, kNorms[i]);
     }
     const Tensor* cos = tensor(p, a[15], "cos", at::kFloat, kWhole);
@@ -253,8 +255,8 @@ PyObject* tokens(PyObject* const* a, Py_ssize_t n, const F& f) {
     const Cache c(p, a + 2, B);
     const Tensor& k = needed(tensor(p, a[0], "k", at::kBFloat16), "k");
     const Tensor& v = needed(tensor(p, a[1], "v", at::kBFloat16), "v");
-    const Tensor* start = tensor(p, a[9], "start", at::kInt);
-    const Tensor* count = tensor(p, a[12], "count", at::kInt);
+    const Tensor* start = tensor(p, a[9], "start", at::kInt, kWhole);
+    const Tensor* count = tensor(p, a[12], "count", at::kInt, kWhole);
     sized(start, B, "start");
     sized(count, B, "count");
     const int64_t w = (int64_t)c.H * c.D, ldk = rows(k, product(B, T), w, "k");
@@ -287,8 +289,8 @@ PyObject* py_attn_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Cache c(p, a + 1, B);
     const Tensor& q = needed(tensor(p, a[0], "q", at::kBFloat16), "q");
     const Tensor& o = needed(tensor(p, a[9], "o", at::kBFloat16), "o");
-    const Tensor* lens = tensor(p, a[8], "lens", at::kInt);
-    const Tensor* q_lens = tensor(p, a[13], "q_lens", at::kInt);
+    const Tensor* lens = tensor(p, a[8], "lens", at::kInt, kWhole);
+    const Tensor* q_lens = tensor(p, a[13], "q_lens", at::kInt, kWhole);
     const Tensor* ws = tensor(p, a[16], "ws", at::kByte, kWhole);
     sized(lens, B, "lens");
     sized(q_lens, B, "q_lens");
@@ -316,7 +318,7 @@ PyObject* py_attn_cross(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& k = needed(tensor(p, a[1], "k", at::kBFloat16), "k");
     const Tensor& v = needed(tensor(p, a[2], "v", at::kBFloat16), "v");
     const Tensor& o = needed(tensor(p, a[3], "o", at::kBFloat16), "o");
-    const Tensor* k_lens = tensor(p, a[10], "k_lens", at::kInt);
+    const Tensor* k_lens = tensor(p, a[10], "k_lens", at::kInt, kWhole);
     const Tensor* mask = tensor(p, a[11], "mask", at::kByte, kWhole, true);
     const Tensor* ws = tensor(p, a[13], "ws", at::kByte, kWhole);
     sized(k_lens, B, "k_lens");
