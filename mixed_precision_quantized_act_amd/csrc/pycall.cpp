@@ -116,6 +116,21 @@ int64_t rows(const Tensor& t, int64_t n, int64_t width, const char* name, int64_
   return std::max(t.stride(0), (t.size(1) + step - 1) / step * step);
 }
 
+// The same for a stride that the caller gives (None: the tensor's own): the
+// last row has to end within the tensor's storage, whatever its shape.  (More
+// rows than the library takes, or smaller strides, it refuses itself.)
+int64_t rows_of(PyObject* given, const Tensor& t, int64_t n, int64_t width, const char* name,
+                int64_t step = 8) {
+  if (given == Py_None) return rows(t, n, width, name, step);
+  const int64_t ld = integer(given), item = (int64_t)t.itemsize();
+  if (n < 1 || n > QA_ROWS_MAX || width < 1 || ld < width) return ld;
+  const int64_t has = (int64_t)t.storage().nbytes() / item - t.storage_offset();
+  if (width > has || (n > 1 && ld > (has - width) / (n - 1)))
+    refuse("%s: %lld rows of %lld elements, %lld apart, do not fit the %lld that it has", name,
+           (long long)n, (long long)width, (long long)ld, (long long)has);
+  return ld;
+}
+
 // The parts of an NVFP4 cache and its table: 7 arguments.
 struct Cache {
   uint8_t* part[4];
@@ -198,8 +213,8 @@ PyObject* py_qlinear_bf16(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     sized(ts, 1, "w_ts");
     sized(bias, N, "bias");
-    const int64_t ldx = a[11] == Py_None ? rows(x, M, K, "x") : integer(a[11]);
-    const int64_t ldy = a[12] == Py_None ? rows(y, M, N, "y", 1) : integer(a[12]);
+    const int64_t ldx = rows_of(a[11], x, M, K, "x");
+    const int64_t ldy = rows_of(a[12], y, M, N, "y", 1);
     return run([&] {
       return f_qlinear_bf16(ptr<uint16_t>(&x), ldx, ptr<uint8_t>(wq), ptr<uint8_t>(ws), ptr<float>(ts),
                             M, N, K, ptr<uint16_t>(bias), ptr<void>(&y), ldy, (qa_out)out, (qa_epi)epi,
