@@ -428,6 +428,7 @@ int qlinear_bf16(const uint16_t* x, int64_t ldx, const uint8_t* w_q, const uint8
  *         v cos + u sin) with cos, sin f32 [P][D / 2] at row pos[m] (int32
  *         [M]; NULL: m), entry i.  A token whose position lies outside
  *         0 .. P - 1 (-1 for the text tokens of a joint sequence) is not turned.
+ *         Both tables or, with P = 0, neither (from Python always both).
  * float32 throughout, one rounding to bf16.  q_out, k_out bf16 [M][ldqo],
  * [M][ldko]; each may be its input itself (same pointer and stride); no
  * other overlap.  All bf16 pointers 16-byte aligned, strides multiples of 8;

@@ -742,7 +742,7 @@ int qk_norm_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int6
   if (int s = check_heads(k, M, ldk, Hk, D)) return s;
   if (int s = check_heads(q_out, M, ldqo, Hq, D)) return s;
   if (int s = check_heads(k_out, M, ldko, Hk, D)) return s;
-  if (rope == QA_ROPE_NONE ? (cos || sin || pos) : (P != 0 && (!cos || !sin))) return QA_EINVAL;
+  if (rope == QA_ROPE_NONE ? (cos || sin || pos) : (!cos != !sin || (P != 0 && !cos))) return QA_EINVAL;
   if (rope != QA_ROPE_NONE && P < 0) return QA_ESHAPE;
   if (!aligned16(q_w) || !aligned16(q_b) || !aligned16(k_w) || !aligned16(k_b)) return QA_EALIGN;
   if (!aligned4(cos) || !aligned4(sin) || !aligned4(pos)) return QA_EALIGN;

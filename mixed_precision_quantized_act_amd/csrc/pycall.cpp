@@ -243,13 +243,15 @@ PyObject* py_qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor* sin = tensor(p, a[16], "sin", at::kFloat, kWhole);
     const Tensor* pos = tensor(p, a[17], "pos", at::kInt, kWhole);
     sized(pos, M, "pos");
+    const int norm = small(a[8], "norm"), rope = small(a[14], "rope");
+    if (rope != QA_ROPE_NONE && !(cos && sin)) refuse("cos, sin: a rotation needs both tables");
     int64_t P = 0;
     if (cos && sin) {
       if (cos->dim() != 2 || cos->sizes() != sin->sizes() || cos->size(1) != D / 2)
         refuse("cos, sin: need shape [P, %d]", D / 2);
       P = cos->size(0);
     }
-    const int norm = small(a[8], "norm"), rope = small(a[14], "rope");
+    if (P == 0 && rope != QA_ROPE_NONE) cos = sin = nullptr;      // (an empty tensor may have no address)
     const float eps = (float)real(a[13]);
     return run([&] {
       return f_qk_norm_rope(ptr<uint16_t>(t[0]), ld[0], H[0], ptr<uint16_t>(t[1]), ld[1], H[1], M, D,
