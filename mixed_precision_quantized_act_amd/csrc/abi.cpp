@@ -58,6 +58,11 @@ bool rows_overlap(const void* a, int64_t lda, int64_t wa, const void* b, int64_t
   return !(r >= wa && r + wb <= lda);
 }
 
+// The same of `n` bytes from p, read as they lie (NULL: none), with the rows at a.
+bool rows_meet(const void* a, int64_t lda, int64_t wa, int64_t Ma, const void* p, int64_t n) {
+  return p && rows_overlap(a, lda, wa, p, lda, (n + 1) / 2, Ma, 1);
+}
+
 int hip_status(hipError_t e) { return e == hipSuccess ? QA_OK : QA_EHIP; }
 
 int check_mk(int64_t M, int64_t K) {
@@ -754,6 +759,13 @@ int qk_norm_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int6
       rows_overlap(k_out, ldko, wk, q, ldq, wq, M, M) ||
       rows_overlap(q_out, ldqo, wq, k_out, ldko, wk, M, M))
     return QA_EALIAS;
+  // (positions are below 2^31)
+  const int64_t table = (P < (int64_t)1 << 31 ? P : (int64_t)1 << 31) * (D / 2) * 4;
+  const struct { const void* p; int64_t n; } read[] = {{q_w, D * 2}, {q_b, D * 2}, {k_w, D * 2}, {k_b, D * 2},
+                                                       {cos, table}, {sin, table}, {pos, M * 4}};
+  for (const auto& r : read)
+    if (rows_meet(q_out, ldqo, wq, M, r.p, r.n) || rows_meet(k_out, ldko, wk, M, r.p, r.n))
+      return QA_EALIAS;
   if (M == 0) return QA_OK;
   const QkArgs a = {q, ldq, k, ldk, M, Hq, Hk, D, norm, rope, q_w, q_b, k_w, k_b,
                     eps, 1.0f / (float)D, cos, sin, P, pos, q_out, ldqo, k_out, ldko};
