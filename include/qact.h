@@ -432,9 +432,8 @@ int qlinear_bf16(const uint16_t* x, int64_t ldx, const uint8_t* w_q, const uint8
  * float32 throughout, one rounding to bf16.  q_out, k_out bf16 [M][ldqo],
  * [M][ldko]; each may be its input itself (same pointer and stride); no
  * other overlap of outputs with anything (QA_EALIAS).  All bf16 pointers
- * 16-byte aligned, strides multiples of 8;
- * cos, sin and pos 4-byte aligned.  D a multiple of 16, 16 .. 256; eps >= 0;
- * 0 <= M < 2^24, M (Hq + Hk) < 2^26.
+ * 16-byte aligned, strides multiples of 8; cos, sin and pos 4-byte aligned.
+ * D a multiple of 16, 16 .. 256; eps >= 0; 0 <= M < 2^24, M (Hq + Hk) < 2^26.
  * ------------------------------------------------------------------------ */
 typedef enum { QA_NORM_NONE = 0, QA_NORM_RMS = 1, QA_NORM_LAYER = 2 } qa_norm;
 typedef enum { QA_ROPE_NONE = 0, QA_ROPE_PAIRS = 1, QA_ROPE_HALVES = 2 } qa_rope;

@@ -144,14 +144,16 @@ qk_norm_rope_kernel(QkArgs a, int qchunks, int chunks, Gate gate) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(x[i] * r, w[i], b[i]);
     }
-    if (a.rope == QA_ROPE_PAIRS) {
+    // (a token that is not turned is passed on: times 1 and 0, an infinite
+    // element would make its partner NaN)
+    if (turn && a.rope == QA_ROPE_PAIRS) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float p = x[2 * i], q = x[2 * i + 1];
         x[2 * i] = __builtin_fmaf(p, cs[i], -(q * sn[i]));
         x[2 * i + 1] = __builtin_fmaf(q, cs[i], p * sn[i]);
       }
-    } else if (a.rope == QA_ROPE_HALVES) {
+    } else if (turn && a.rope == QA_ROPE_HALVES) {
       const bool upper = 8 * l >= D / 2;
       const int other = (lane & ~(LPH - 1)) | ((upper ? l - D / 16 : l + D / 16) & (LPH - 1));
 #pragma unroll
