@@ -478,7 +478,8 @@ int qk_norm_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int6
  *   rows; the rows behind them are neither read nor written.  causal != 0:
  *   the last query row stands at position lens[b] - 1 and a row sees no
  *   position after its own.  A row that sees nothing gives zeros.  Slots
- *   that are not seen may hold any bytes.
+ *   that are not seen may hold any bytes.  A k_ts that is not finite makes NaN
+ *   of every row that sees a position.
  *   D 64 or 128; Hq a multiple of H; scale > 0; B Lq Hq < 2^24.
  *   ws: with attn_kv4_workspace() bytes a call with few query rows splits
  *   the keys over more workgroups; less (also none) splits less.  The sums

@@ -228,27 +228,39 @@ struct CrossSource {
 // to a largest value in [1, 2) (an element below 2^-24 of it is lost, one
 // below 2^-17 keeps fewer bits: less than the float32 sum's own rounding);
 // the exponent returns through `c`, which turns a product into a logit in
-// units of log2.  N pieces of 8 elements per lane; `most` combines the
-// lanes that hold one row.
+// units of log2.  c is a positive number: the sign of the keys' tensor scale goes
+// to the row, and where the scale is not finite, or c not a float32, the row is
+// NaN, so that rows that see nothing still give zeros.  N pieces of 8 elements per
+// lane; `most` combines the lanes that hold one row.
 template <bool F16, int N, class Most>
 __device__ __forceinline__ float query_operand(u32x4 (&q)[N], float scale_log2e, float k_scale,
                                                Most most) {
+  float c = scale_log2e;
+  if constexpr (F16) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = max(top, fold_max(abs_max8_pk(q[i], u16x2{0, 0})));
+    // the exponent field alone; a row of zeros, infinities or NaN stays as it is
+    const uint32_t e = __float_as_uint(most(__uint_as_float(top << 16))) >> 23;
+    const int ex = e == 0 || e == 255 ? 0 : (int)e - 127;
+    const uint32_t sign = k_scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        q[i][j] = f16_pack(__builtin_ldexpf(bf16_lo(q[i][j]), -ex),
+                           __builtin_ldexpf(bf16_hi(q[i][j]), -ex)) ^ sign;
+    c = __builtin_ldexpf(scale_log2e, ex) * fabsf(k_scale);
+  }
+  if (!(c < INFINITY)) {
+    const uint32_t nan = F16 ? 0x7E007E00u : 0x7FC07FC0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = u32x4{nan, nan, nan, nan};
+    c = 1.0f;
+  }
   // (at least the smallest normal number: a product of minus infinity, what
   // is not seen, with it stays minus infinity)
-  if constexpr (!F16) return fmaxf(scale_log2e, 0x1p-126f);
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) top = max(top, fold_max(abs_max8_pk(q[i], u16x2{0, 0})));
-  // the exponent field alone; a row of zeros, infinities or NaN stays as it is
-  const uint32_t e = __float_as_uint(most(__uint_as_float(top << 16))) >> 23;
-  const int ex = e == 0 || e == 255 ? 0 : (int)e - 127;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      q[i][j] = f16_pack(__builtin_ldexpf(bf16_lo(q[i][j]), -ex),
-                         __builtin_ldexpf(bf16_hi(q[i][j]), -ex));
-  return fmaxf(__builtin_ldexpf(scale_log2e, ex) * k_scale, 0x1p-126f);
+  return fmaxf(c, 0x1p-126f);
 }
 
 // --------------------------------------------------------- split of the keys --
