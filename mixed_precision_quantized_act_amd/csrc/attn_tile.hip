@@ -9,18 +9,12 @@
 // them: 157 us.  Counters: VALU busy 0.42 of the cycles, MFMA 0.31, both waves of
 // a SIMD waiting for data or each other a third of the time.  Why 8 waves: with 4
 // a tile is staged for half as many rows (195 us; 3 of them per SIMD spill, 190).
+#include "attn_cuts.h"
 #include "attn_rows.h"
 
 namespace qact {
 
 namespace {
-
-// How a row tile's keys are cut: n pieces, each `size` parts of `whole` and
-// the last one what is left.
-constexpr int kCuts = 64;
-struct Pieces {
-  int n, size, whole;
-};
 
 // Staging by T threads: a thread takes kPer units, each of K or of V, the same
 // for a whole wave.  A unit is loaded a tile before it is stored; both are
@@ -167,8 +161,7 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, Pieces pc, Gat
   const int last = min(tile * (32 * W) + 32 * W, rows) - 1;
   const int end = src.causal ? n - (nq - 1 - last / G) : n;
   const int chunks = (max(end, 0) + kTileKeys - 1) / kTileKeys;
-  const int c0 = (int)((int64_t)chunks * (piece * pc.size) / pc.whole);
-  const int c1 = piece == pc.n - 1 ? chunks : (int)((int64_t)chunks * ((piece + 1) * pc.size) / pc.whole);
+  const int c0 = piece_begin(pc, chunks, piece), c1 = piece_end(pc, chunks, piece);
   const int base0 = c0 * kTileKeys, nt = c1 - c0;
   // tiles of which this wave's rows see anything
   const int mine = min(nt, max(0, (wend - base0 + kTileKeys - 1) / kTileKeys));
@@ -329,58 +322,18 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, Pieces pc, Gat
 constexpr int kTileWaves = 8;
 constexpr int kTileRows = 32 * kTileWaves;
 
-// One workgroup fits a compute unit: this many run at once.  Row tiles that do
-// not fill them (or fill them badly) have their keys cut into pieces: n equal
-// ones, or n - 1 large ones that all run at once and a small one for the places
-// that are left, which take k of those each.  The cost in us: the time of the
-// slowest place, a workgroup being kTileStart and kTileTime a tile of keys, and for
-// more than one piece the partial sums, written and read again, and the launch
-// that joins them.  (1350 rows, 30 heads of 64, 12376 keys: 180 row tiles, so one
-// piece leaves 76 places idle.  Two pieces, the large one 0.70, 0.75, 0.80 and
-// 0.85 of the keys: 218, 187, 181 and 190 us; 3, 4 and 7 equal ones: 237, 190 and
-// 203.)
-constexpr int64_t kPlaces = 256;
-constexpr double kTileStart = 8.0;
-template <int D>
-constexpr double kTileTime = D == 64 ? 0.97 : 1.7;
-
-Pieces pieces_of(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L, size_t ws_bytes) {
+Pieces cut_of(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L, size_t ws_bytes) {
   const int64_t rows = B * Lq * Hq;
   const int64_t u = B * Hkv * ((Lq * (Hq / Hkv) + kTileRows - 1) / kTileRows);
-  const int64_t chunks = (L + kTileKeys - 1) / kTileKeys;
-  const double T = (double)chunks * (D == 64 ? kTileTime<64> : kTileTime<128>);
-  const int64_t fit = (int64_t)(ws_bytes / AttnSplit::bytes(rows, D));
-  Pieces best = {1, 1, 1};
-  double least = 0.0;
-  for (int n = 1; n <= 16; ++n) {
-    if (n > 1 && (n > fit || n > chunks)) break;
-    const double joined = n > 1 ? 4.0 + (double)n * (double)rows * D * 4 * 1.5 / 4e6 : 0.0;
-    const double equal = (double)((u * n + kPlaces - 1) / kPlaces) * (T / n + kTileStart) + joined;
-    if (n == 1 || equal < least) {
-      least = equal;
-      best = {n, 1, n};
-    }
-    const int64_t left = kPlaces - u * (n - 1);               // places beside the large pieces
-    if (n < 2 || left <= 0) continue;
-    const double k = (double)((u + left - 1) / left);
-    // the large part f for which both kinds of places take the same time
-    const double f = (k + (k - 1.0) * kTileStart / T) / (1.0 + k * (n - 1));
-    const int size = (int)(f * kCuts + 0.5);
-    if (size * (n - 1) >= kCuts) continue;
-    const double uneven = f * T + kTileStart + joined;
-    if (uneven < least) {
-      least = uneven;
-      best = {n, size, kCuts};
-    }
-  }
-  return best;
+  return pieces_of(u, rows, D, (L + kTileKeys - 1) / kTileKeys,
+                   (int64_t)(ws_bytes / AttnSplit::bytes(rows, D)));
 }
 
 }  // namespace
 
 // (asked for: at most 32 MiB, whatever more pieces would give)
 size_t attn_tile_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
-  const Pieces p = pieces_of(B, Lq, Hq, Hkv, D, L, (size_t)32 << 20);
+  const Pieces p = cut_of(B, Lq, Hq, Hkv, D, L, (size_t)32 << 20);
   return p.n > 1 ? p.n * AttnSplit::bytes(B * Lq * Hq, D) : 0;
 }
 
@@ -389,7 +342,7 @@ hipError_t launch_attn_tile(const AttnArgs& a, const Source& src, int64_t L, voi
                             size_t ws_bytes, hipStream_t stream) {
   const Gate gt = current_gate();
   const int64_t rows = a.B * a.Lq * a.Hq;
-  const Pieces pc = pieces_of(a.B, a.Lq, a.Hq, a.Hkv, a.D, L, ws_bytes);
+  const Pieces pc = cut_of(a.B, a.Lq, a.Hq, a.Hkv, a.D, L, ws_bytes);
   const AttnSplit sp = AttnSplit::in(ws, pc.n, rows, a.D);
   const int64_t tiles = (a.Lq * (a.Hq / a.Hkv) + kTileRows - 1) / kTileRows;
   const dim3 grid((unsigned)(a.B * a.Hkv * pc.n * tiles));
