@@ -1,5 +1,6 @@
 """Build libqact.so (the HIP kernels and the C ABI) for gfx950 with hipcc, and
-_call.so (the compiled Python calls) with the host compiler.
+_call.so (the compiled Python calls) with the host compiler, where there is one
+and PyTorch.
 
 Run as ``python -m mixed_precision_quantized_act_amd.build`` or through
 ``__graft_entry__.build()``.  Each source compiles to its own object in
@@ -50,11 +51,12 @@ def _run(cmd):
 
 
 def call_command(out):
-    """The compiler's line for _call.so (it finds PyTorch's libraries loaded)."""
-    cxx = shutil.which("g++") or shutil.which("c++")
-    if not cxx:
-        raise RuntimeError("no host C++ compiler found")
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    """The compiler's line for _call.so (it finds PyTorch's libraries loaded);
+    None without PyTorch or a host compiler."""
+    cxx, spec = shutil.which("g++") or shutil.which("c++"), importlib.util.find_spec("torch")
+    if not cxx or not spec:
+        return None
+    torch = os.path.dirname(spec.origin)
     rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
     include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]
@@ -72,20 +74,26 @@ def build(verbose=True):
         obj = os.path.join(OBJ_DIR, os.path.splitext(src)[0] + ".o")
         jobs.append(([cc] + FLAGS + ["-c", os.path.join(CSRC, src), "-o", obj], obj))
     call = call_command(CALL + ".tmp")
-    commands = [call] + [cmd for cmd, _ in jobs]
+    commands = [cmd for cmd, _ in jobs]
     if verbose:
-        for cmd in commands:
+        for cmd in ([call] if call else []) + commands:
             print(" ".join(cmd), flush=True)
-    workers = max(1, min(len(commands), os.cpu_count() or 1))
-    with ThreadPoolExecutor(max_workers=workers) as ex:
-        list(ex.map(_run, commands))
-    os.replace(CALL + ".tmp", CALL)
     tmp = LIB + ".tmp"
     link = [cc, "--offload-arch=gfx950", "-shared", "-fPIC"] + [o for _, o in jobs] + ["-o", tmp]
-    if verbose:
-        print(" ".join(link), flush=True)
-    _run(link)
-    os.replace(tmp, LIB)
+    workers = max(1, min(len(commands) + 1, os.cpu_count() or 1))
+    with ThreadPoolExecutor(max_workers=workers) as ex:
+        # (the library does not wait for the Python calls, nor fail with them)
+        called = ex.submit(_run, call) if call else None
+        list(ex.map(_run, commands))
+        if verbose:
+            print(" ".join(link), flush=True)
+        _run(link)
+        os.replace(tmp, LIB)
+    if called:
+        called.result()
+        os.replace(CALL + ".tmp", CALL)
+    else:
+        print("no PyTorch or no host C++ compiler: the library alone, without _call.so", flush=True)
     return LIB
 
 
