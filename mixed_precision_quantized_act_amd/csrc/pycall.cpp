@@ -96,6 +96,13 @@ template <class T>
 T* ptr(const Tensor* t) {
   return t ? static_cast<T*>(t->data_ptr()) : nullptr;
 }
+// The same where the library wants an address even with nothing to read or write
+// (no rows, no columns): that of an aligned place for a tensor without elements.
+template <class T>
+T* place(const Tensor* t) {
+  alignas(16) static char none[16];
+  return t && t->numel() == 0 ? reinterpret_cast<T*>(none) : ptr<T>(t);
+}
 void sized(const Tensor* t, int64_t n, const char* name) {
   if (t && t->numel() < n)
     refuse("%s: needs %lld elements, got %lld", name, (long long)n, (long long)t->numel());
@@ -216,8 +223,8 @@ PyObject* py_qlinear_bf16(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t ldx = rows_of(a[11], x, M, K, "x");
     const int64_t ldy = rows_of(a[12], y, M, N, "y", 1);
     return run([&] {
-      return f_qlinear_bf16(ptr<uint16_t>(&x), ldx, ptr<uint8_t>(wq), ptr<uint8_t>(ws), ptr<float>(ts),
-                            M, N, K, ptr<uint16_t>(bias), ptr<void>(&y), ldy, (qa_out)out, (qa_epi)epi,
+      return f_qlinear_bf16(place<uint16_t>(&x), ldx, place<uint8_t>(wq), place<uint8_t>(ws), ptr<float>(ts),
+                            M, N, K, ptr<uint16_t>(bias), place<void>(&y), ldy, (qa_out)out, (qa_epi)epi,
                             p.stream);
     });
   });
