@@ -235,7 +235,6 @@ struct CrossSource {
 template <bool F16, int N, class Most>
 __device__ __forceinline__ float query_operand(u32x4 (&q)[N], float scale_log2e, float k_scale,
                                                Most most) {
-  float c = scale_log2e;
   if constexpr (F16) {
     uint32_t top = 0;
 #pragma unroll
@@ -243,19 +242,23 @@ __device__ __forceinline__ float query_operand(u32x4 (&q)[N], float scale_log2e,
     // the exponent field alone; a row of zeros, infinities or NaN stays as it is
     const uint32_t e = __float_as_uint(most(__uint_as_float(top << 16))) >> 23;
     const int ex = e == 0 || e == 255 ? 0 : (int)e - 127;
-    const uint32_t sign = k_scale < 0.0f ? 0x80008000u : 0u;
+    const float c = __builtin_ldexpf(scale_log2e, ex) * fabsf(k_scale);
+    // (times 1, -1 or NaN, not a branch: 16 heads of 128, 1350 rows, 12376 keys: 175.9
+    // -> 173.6 us)
+    const bool good = c < INFINITY;
+    const float sign = good ? copysignf(1.0f, k_scale) : __builtin_nanf("");
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        q[i][j] = f16_pack(__builtin_ldexpf(bf16_lo(q[i][j]), -ex),
-                           __builtin_ldexpf(bf16_hi(q[i][j]), -ex)) ^ sign;
-    c = __builtin_ldexpf(scale_log2e, ex) * fabsf(k_scale);
+        q[i][j] = f16_pack(__builtin_ldexpf(bf16_lo(q[i][j]), -ex) * sign,
+                           __builtin_ldexpf(bf16_hi(q[i][j]), -ex) * sign);
+    return fmaxf(good ? c : 1.0f, 0x1p-126f);
   }
+  float c = scale_log2e;
   if (!(c < INFINITY)) {
-    const uint32_t nan = F16 ? 0x7E007E00u : 0x7FC07FC0u;
 #pragma unroll
-    for (int i = 0; i < N; ++i) q[i] = u32x4{nan, nan, nan, nan};
+    for (int i = 0; i < N; ++i) q[i] = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
     c = 1.0f;
   }
   // (at least the smallest normal number: a product of minus infinity, what

@@ -82,3 +82,28 @@ def test_logits_beyond_float32_leave_rows_without_keys_alone(Lq):
     for b, n in enumerate(LENS):
         sees = n - (Lq - 1 - np.arange(Lq)) > 0
         assert np.all(got[b][~sees] == 0)
+
+
+@pytest.mark.parametrize("Lq", [1, 20, 300])
+@pytest.mark.parametrize("Lk", [100, 700])
+@pytest.mark.parametrize("scale", [3e38, 1e-38])
+def test_states_with_the_largest_and_smallest_scale(Lq, Lk, scale):
+    """Sequences that see nothing give zeros; with logits near zero the others give the average of what they see."""
+    qa, t = _qa(), torch()
+    g = rng(706, Lq, Lk)
+    q, k, v = (bits(g.standard_normal((3 * n, 128))) for n in (Lq, Lk, Lk))
+    m = np.ones((3, Lk), np.uint8)
+    m[1] = 0
+    o = t.full((3 * Lq, 128), 7.0, dtype=t.bfloat16, device="cuda")
+    qd, kd, vd = (dev(x).view(t.bfloat16) for x in (q, k, v))
+    ws = t.full((max(qa.attn_cross_workspace(3, Lq, Lk, 2, 2, 64), 16),), 0xFF, dtype=t.uint8, device="cuda")
+    qa.attn_cross(qd, kd, vd, o, 3, Lq, Lk, 2, 2, 64, mask=dev(m), k_lens=dev(np.array([Lk, Lk, 60], np.int32)),
+                  scale=scale, ws=ws)
+    t.cuda.synchronize()
+    got = val(host(o)).reshape(3, Lq, 2, 64)
+    assert np.all(got[1] == 0)
+    if scale < 1:
+        for b, n in ((0, Lk), (2, 60)):
+            vv = val(v).reshape(3, Lk, 2, 64)[b, :n]
+            want, spread = vv.mean(0), np.abs(vv).mean(0)
+            assert np.all(np.abs(got[b] - want) <= attn_tol(want, spread, 0.0, 64, Lk, 2.0 ** -8, 0.0))
