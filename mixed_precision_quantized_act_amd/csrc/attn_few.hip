@@ -16,8 +16,8 @@
 // rows cost no more than one.
 //
 // 16 streams of 16384 to 32768 tokens, one query token each, 32 query and 8 key
-// heads of 128: 90 us and 4.6 for the join, 463 MB at 5.1 TB/s.  24 tokens to 300 to
-// 1500 bf16 states, 20 heads of 64: 24 us and 4.4.
+// heads of 128: 92 us and 4.7 for the join in a kernel trace, 463 MB at 5.0 TB/s.  24
+// tokens to 300 to 1500 bf16 states, 20 heads of 64: 25 us and 4.8.
 #include "attn_common.h"
 
 namespace qact {

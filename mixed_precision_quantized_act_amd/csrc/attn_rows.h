@@ -1,7 +1,7 @@
 // Many query rows: what a wave does with 32 of them over tiles of 64 staged
 // keys.
 //
-// VALU and MFMA bound it alike: for heads of 64 the weights of 32 keys take about
+// VALU and MFMA weigh alike: for heads of 64 the weights of 32 keys take about
 // 118 ns of a SIMD (16 exp2 at 4.4, 24 other instructions at 2.0), the two
 // products' MFMAs and the sums' 123.  Both run at once only when ONE wave's
 // instructions alternate between them (an MFMA and up to 7 VALU instructions: the
@@ -9,6 +9,8 @@
 // the weights of 32 keys while its MFMAs compute the logits of the next 32 and the
 // second product of the 32 before.  Alternating so, with operands read from shared
 // memory, a step takes 206 ns of a SIMD that two waves share.
+// Over a whole launch neither unit is busy half of the time (VALU 0.45 and MFMA 0.34
+// of the cycles, attn_tile.hip): what is left are the waits around the steps.
 //
 // For the same reason the VALU is left with as little else as possible: no
 // maximum is taken of most tiles.  The weights are formed to the reference that

@@ -4,9 +4,10 @@
 // rows, 32 at a time, without meeting again; the next 32 are on their way
 // meanwhile.  attn_rows.h says what a wave does with them.
 //
-// 30 heads of 64, 17550 query tokens, 226 states: 56 us, 0.50 us of a SIMD for
+// 30 heads of 64, 17550 query tokens, 226 states: 52 us a call (58 in a kernel trace,
+// which slows it), 0.50 us of a SIMD for
 // 32 rows by 64 keys (the alternating products and weights alone take 0.41 us
-// of it) and about 20 us for the rest: launch, staging, each block's first and
+// of it) and about 16 us for the rest: launch, staging, each block's first and
 // last products and its rows' load and store.  A memory that is read and written
 // once would take 27 us.  12 waves instead of 8 spill registers and cost 6 us
 // more.

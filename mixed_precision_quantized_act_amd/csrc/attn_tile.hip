@@ -4,10 +4,11 @@
 // expanded once for all rows), ahead of what its MFMAs read.  attn_rows.h says
 // what a wave does with them and what bounds it.
 //
-// 1350 rows to 12376 tokens of a cache, 30 heads of 64: 179 us with the join, 128
-// GFLOP at 0.72 PFLOP/s (a large library product: 1.21); heads of 128, 16 of
-// them: 157 us.  Counters: VALU busy 0.42 of the cycles, MFMA 0.31, both waves of
-// a SIMD waiting for data or each other a third of the time.  Why 8 waves: with 4
+// 1350 rows to 12376 tokens of a cache, 30 heads of 64: 178 us a call, 128 GFLOP at
+// 0.72 PFLOP/s (a large library product: 1.21); in a kernel trace, which slows
+// both, 178 for this kernel and 7 for the join.  Heads of 128, 16 of them: 173 us.
+// Counters: VALU busy 0.45 of the cycles, MFMA 0.34, a wave waiting for data or the
+// others a third of its time, 1.6 of 2 waves on a SIMD.  Why 8 waves: with 4
 // a tile is staged for half as many rows (195 us; 3 of them per SIMD spill, 190).
 #include "attn_cuts.h"
 #include "attn_rows.h"
@@ -141,7 +142,7 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, Pieces pc, Gat
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // causal: the tiles with most keys first, of all heads, so that the short ones
-  // fill the end (4096 rows of 32 heads of 64 over themselves: 150 -> 89 us)
+  // fill the end (4096 rows of 32 heads of 64 over themselves: 153 -> 100 us)
   const int others = gridDim.x / tiles;
   const int tile = src.causal ? tiles - 1 - blockIdx.x / others : blockIdx.x % tiles;
   const int at = src.causal ? blockIdx.x % others : blockIdx.x / tiles, hk = at % a.Hkv;
