@@ -88,6 +88,9 @@ def build(verbose=True):
         if verbose:
             print(" ".join(link), flush=True)
         _run(link)
+        # (calls that were built for another library's functions do not stay)
+        if os.path.exists(CALL):
+            os.remove(CALL)
         os.replace(tmp, LIB)
     if called:
         called.result()

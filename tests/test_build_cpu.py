@@ -62,3 +62,26 @@ def test_calls_that_do_not_compile_leave_the_library(commands, monkeypatch):
     with pytest.raises(RuntimeError):
         b.build(verbose=False)
     assert os.path.exists(b.LIB) and not os.path.exists(b.CALL)
+
+
+@pytest.mark.parametrize("missing", ["compiler", "success"])
+def test_calls_of_an_older_library_do_not_stay(commands, monkeypatch, missing):
+    """A _call.so that is there was built against the functions of the library that is replaced."""
+    pytest.importorskip("torch")
+    monkeypatch.setattr(b.shutil, "which", lambda name: None if missing == "compiler" else "/usr/bin/" + name)
+    with open(b.CALL, "w") as f:
+        f.write("older")
+    run = b._run
+
+    def fails(cmd):
+        if _calls([cmd]):
+            raise RuntimeError("compiler failed")
+        run(cmd)
+
+    if missing == "success":
+        monkeypatch.setattr(b, "_run", fails)
+        with pytest.raises(RuntimeError):
+            b.build(verbose=False)
+    else:
+        b.build(verbose=False)
+    assert os.path.exists(b.LIB) and not os.path.exists(b.CALL)
