@@ -414,6 +414,25 @@ int qlinear_bf16(const uint16_t* x, int64_t ldx, const uint8_t* w_q, const uint8
                  int64_t ldy, qa_out out, qa_epi epi, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * qlinear_w8a8: the linear of INT8 activations against an INT8 weight, for
+ * layers whose weights are kept in 8 bits (6Bit-Diffusion, abstract: INT8 for
+ * the volatile layers).
+ *   y[m][n] = a_s[m] w_s[n] sum_k a[m][k] w[n][k] (+ bias[n]) (-> GELU-tanh)
+ * a_q i8 [M][K], a_s f32 [M] and w_q i8 [N][K], w_s f32 [N], as act_quant INT8
+ * makes both (any codes, -128 too; a_q, w_q 16-byte aligned); bias, y, out and
+ * epi as for qlinear_nvfp4.  The sum is an exact int32; it is rounded once to
+ * float32, then multiplied by w_s[n] and by a_s[m] (one rounding each), + bias.
+ * K a multiple of 16 below 2^17 (QA_ESHAPE otherwise), M and N as for
+ * qlinear_nvfp4.  ws: with qlinear_w8a8_workspace() bytes (0 for many sizes) the
+ * sums of few output tiles are split along K; less (also none) splits less, with
+ * the same results bit for bit.
+ * ------------------------------------------------------------------------ */
+size_t qlinear_w8a8_workspace(int64_t M, int64_t N, int64_t K);
+int qlinear_w8a8(const int8_t* a_q, const float* a_s, const int8_t* w_q, const float* w_s, int64_t M,
+                 int64_t N, int64_t K, const uint16_t* bias, void* y, int64_t ldy, qa_out out,
+                 qa_epi epi, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * qk_norm_rope: the norm of each query and key head and its rotation by the
  * token's position, in one pass, between a block's QKV linear and its
  * attention.
@@ -442,6 +461,45 @@ int qk_norm_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int6
                  const uint16_t* k_w, const uint16_t* k_b, float eps, qa_rope rope,
                  const float* cos, const float* sin, int64_t P, const int32_t* pos,
                  uint16_t* q_out, int64_t ldqo, uint16_t* k_out, int64_t ldko, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * qk_rope: query and key heads turned by their tokens' positions, the angles
+ * formed in the call, for models that turn a part of each head or stretch
+ * their positions to long contexts (qk_norm_rope turns whole heads by tables).
+ *   (u, v) -> scale (u cos a - v sin a, v cos a + u sin a),  a = pos[m] freq[i]
+ * for the pairs (2 i, 2 i + 1) (QA_ROPE_PAIRS) or (i, i + R / 2)
+ * (QA_ROPE_HALVES), i < R / 2, of a head's first R elements; the other D - R are
+ * passed on.  q, k, q_out, k_out as for qk_norm_rope (each output may be its
+ * input itself).  pos int32 [M] (NULL: m); a token whose position is negative
+ * is passed on.  freq f64 [R / 2] device, radians per position (8-byte aligned;
+ * qa_rope_freqs makes them).  Angles are formed and reduced in float64, sines,
+ * cosines (times scale) and products in float32, one rounding to bf16; elements
+ * that are passed on keep their bits.
+ * D, R multiples of 16, 16 <= R <= D <= 256; scale finite; 0 <= M < 2^24, M (Hq
+ * + Hk) < 2^26; Hq + Hk <= 65536.
+ *
+ * qa_rope_freqs (host arrays, no GPU work): the frequencies of R / 2 pairs.
+ *   QA_STRETCH_NONE    f_i = base^(-2 i / R)
+ *   QA_STRETCH_LINEAR  f_i / factor (positions interpolated)
+ *   QA_STRETCH_BASE    the base times factor^(R / (R - 2)): the slowest pair is
+ *                      stretched by factor, the fastest not at all (R > 2)
+ *   QA_STRETCH_RAMP    (Peng et al., arXiv 2309.00071) a pair that turns more than
+ *                      `fast` times over the `original` positions keeps f_i, one
+ *                      that turns fewer than `slow` times takes f_i / factor, and
+ *                      between them the share of f_i / factor rises linearly with
+ *                      i: c(t) = R ln(original / (2 pi t)) / (2 ln base), from
+ *                      max(floor c(fast), 0) to min(ceil c(slow), R - 1) (at least
+ *                      0.001 further); *scale = 0.1 ln(factor) + 1 where factor > 1.
+ * *scale (nullable) is 1 otherwise.  base > 1, factor >= 1, R even, 2 <= R <=
+ * 65536; RAMP: original > 0, fast >= slow > 0.  original, fast and slow are not
+ * read otherwise.
+ * ------------------------------------------------------------------------ */
+typedef enum { QA_STRETCH_NONE = 0, QA_STRETCH_LINEAR = 1, QA_STRETCH_BASE = 2, QA_STRETCH_RAMP = 3 } qa_stretch;
+int qk_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int64_t ldk, int Hk, int64_t M,
+            int D, int R, qa_rope rope, const double* freq, float scale, const int32_t* pos,
+            uint16_t* q_out, int64_t ldqo, uint16_t* k_out, int64_t ldko, hipStream_t stream);
+int qa_rope_freqs(qa_stretch kind, int R, double base, double factor, double original, double fast,
+                  double slow, double* freq, float* scale);
 
 /* ------------------------------------------------------------------------
  * A key/value cache in NVFP4 (9/16 byte per element) and attention over it,
@@ -506,6 +564,35 @@ int attn_kv4(const uint16_t* q, int64_t ldq, int64_t B, int64_t Lq, int Hq, int 
              const int32_t* table, int64_t max_pages, const int32_t* lens, const int32_t* q_lens,
              int causal, float scale, uint16_t* o, int64_t ldo, void* ws, size_t ws_bytes,
              hipStream_t stream);
+
+/* attn_kv4_tree: attn_kv4 for a tree of drafted tokens that are checked in one
+ * step.  Stream b's q_lens[b] (NULL: Lq) query rows are the last q_lens[b]
+ * positions of its cache (appended before the call): row t stands for drafted
+ * token t at position lens[b] - q_lens[b] + t.  It sees every position before
+ * the drafted ones, and drafted token j where bit j % 64 of word
+ * tree[b tree_stride + t W + j / 64] is set, W = ceil(Lq / 64) (u64, 8-byte
+ * aligned; tree_stride in words, at least Lq W, or 0: one tree for all streams).
+ * Bits of tokens from q_lens[b] on are ignored; a row that sees nothing gives
+ * zeros.  Lq <= 1024.  Everything else, the workspace too, as for attn_kv4.
+ *
+ * kv4_keep: the tokens of a checked tree that are kept move to the front of the
+ * drafted positions: the codes and scales of position start[b] + path[b T + i]
+ * go to position start[b] + i, i < count[b] (int32 [B]; NULL: T; at most T), keys
+ * and values of all heads, as if all were read before any is written (so path may
+ * name a position twice, in any order).  Where either position has no slot
+ * nothing is written; every other slot stays as it was.  path int32 [B][T].
+ * 0 <= T <= 1024, B H < 2^24.  Streams that share a page that is written here
+ * leave a mix of their tokens there. */
+size_t attn_kv4_tree_workspace(int64_t B, int64_t Lq, int Hq, int H, int D, int64_t max_len);
+int attn_kv4_tree(const uint16_t* q, int64_t ldq, int64_t B, int64_t Lq, int Hq, int H, int D,
+                  const uint8_t* k_q, const uint8_t* k_s, const uint8_t* v_q, const uint8_t* v_s,
+                  const float* k_ts, const float* v_ts, int64_t pages, int page,
+                  const int32_t* table, int64_t max_pages, const int32_t* lens,
+                  const int32_t* q_lens, const uint64_t* tree, int64_t tree_stride, float scale,
+                  uint16_t* o, int64_t ldo, void* ws, size_t ws_bytes, hipStream_t stream);
+int kv4_keep(uint8_t* k_q, uint8_t* k_s, uint8_t* v_q, uint8_t* v_s, int64_t B, int64_t T, int H, int D,
+             int64_t pages, int page, const int32_t* table, int64_t max_pages, const int32_t* start,
+             const int32_t* path, const int32_t* count, hipStream_t stream);
 
 /* attn_cross: attention of bf16 queries to an encoder's states of another
  * length (a video block's tokens to the prompt's).  q, o as for attn_kv4; k,

@@ -15,6 +15,7 @@ OUT_BF16, OUT_F32 = 0, 1
 EPI_NONE, EPI_GELU_TANH = 0, 1
 NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 ROPE_NONE, ROPE_PAIRS, ROPE_HALVES = 0, 1, 2
+STRETCH_NONE, STRETCH_LINEAR, STRETCH_BASE, STRETCH_RAMP = 0, 1, 2, 3
 ROWS_MAX = 32                        # QA_ROWS_MAX
 TSCALE_GIVEN = 1
 AMAX_GIVEN = 2
@@ -99,6 +100,15 @@ _SIGS = {
     "attn_cross_workspace": (_SZ, [_I64, _I64, _I64, _I, _I, _I]),
     "attn_cross": (_I, [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _I, _I, _I, _P, _P,
                         ctypes.c_float, _P, _I64, _P, _SZ, _P]),
+    "qlinear_w8a8_workspace": (_SZ, [_I64, _I64, _I64]),
+    "qlinear_w8a8": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _I64, _I, _I, _P, _SZ, _P]),
+    "qk_rope": (_I, [_P, _I64, _I, _P, _I64, _I, _I64, _I, _I, _I, _P, ctypes.c_float, _P, _P, _I64,
+                     _P, _I64, _P]),
+    "qa_rope_freqs": (_I, [_I, _I] + [ctypes.c_double] * 5 + [_P, _P]),
+    "attn_kv4_tree_workspace": (_SZ, [_I64, _I64, _I, _I, _I, _I64]),
+    "attn_kv4_tree": (_I, [_P, _I64, _I64, _I64, _I, _I, _I, _P, _P, _P, _P, _P, _P, _I64, _I, _P, _I64,
+                           _P, _P, _P, _I64, ctypes.c_float, _P, _I64, _P, _SZ, _P]),
+    "kv4_keep": (_I, [_P, _P, _P, _P, _I64, _I64, _I, _I, _I64, _I, _P, _I64, _P, _P, _P, _P]),
     "qa_gamma_from_sums": (ctypes.c_double, [_P]),
     "qa_rel_l2_from_sums": (ctypes.c_double, [_P]),
     "qa_rel_err_from_sums": (ctypes.c_double, [_P]),
@@ -396,6 +406,8 @@ def _native():
                               "python -m mixed_precision_quantized_act_amd.build") from e
         m.bind(*(ctypes.cast(getattr(h, n), ctypes.c_void_p).value for n in (
             "qlinear_bf16", "qk_norm_rope", "kv4_append", "kv4_read", "attn_kv4", "attn_cross")))
+        m.bind_step(*(ctypes.cast(getattr(h, n), ctypes.c_void_p).value for n in (
+            "qlinear_w8a8", "qk_rope", "attn_kv4_tree", "kv4_keep")))
         _call = m
     return _call
 
@@ -406,6 +418,41 @@ def qlinear_bf16(x, w_q, w_s, w_ts, y, M, N, K, bias=None, out=OUT_BF16, epi=EPI
     status = _native().qlinear_bf16(x, w_q, w_s, w_ts, y, M, N, K, bias, out, epi, ldx, ldy, stream)
     if status:
         _check("qlinear_bf16", status)
+
+
+def qlinear_w8a8_workspace(M, N, K):
+    return lib().qlinear_w8a8_workspace(M, N, K)
+
+
+def qlinear_w8a8(a_q, a_s, w_q, w_s, y, M, N, K, bias=None, out=OUT_BF16, epi=EPI_NONE, ldy=None,
+                 ws=None, stream=None):
+    """The linear of INT8 activations a_q [M, K], a_s [M] against an INT8
+    weight w_q [N, K], w_s [N] (act_quant INT8 makes both); exact int32 sums."""
+    status = _native().qlinear_w8a8(a_q, a_s, w_q, w_s, y, M, N, K, bias, out, epi, ldy, ws, stream)
+    if status:
+        _check("qlinear_w8a8", status)
+
+
+def qk_rope(q, k, q_out, k_out, M, Hq, Hk, D, R, freq, rope=ROPE_HALVES, scale=1.0, pos=None,
+            stream=None):
+    """The first R elements of every query head of q [M, Hq * D] and key head
+    of k [M, Hk * D] (bf16, rows of any stride; None without heads) turned by
+    the angles pos[m] * freq[i] (int32; None: m; negative: not turned; float64
+    [R / 2], device) and times scale, into q_out and k_out, which may be q and k."""
+    status = _native().qk_rope(q, k, q_out, k_out, M, Hq, Hk, D, R, freq, rope, scale, pos, stream)
+    if status:
+        _check("qk_rope", status)
+
+
+def rope_freqs(R, base=10000.0, stretch=STRETCH_NONE, factor=1.0, original=0, fast=32.0, slow=1.0):
+    """(frequencies, scale) for qk_rope: float64 [R / 2] host array, radians per
+    position, stretched to `factor` times the context; STRETCH_RAMP: of `original`
+    positions."""
+    import numpy as np
+    freq, scale = np.zeros(max(R, 0) // 2), ctypes.c_float()
+    _check("qa_rope_freqs", lib().qa_rope_freqs(stretch, R, base, factor, original, fast, slow,
+                                                freq.ctypes.data, ctypes.addressof(scale)))
+    return freq, scale.value
 
 
 def qk_norm_rope(q, k, q_out, k_out, M, Hq, Hk, D, norm=NORM_LAYER, q_w=None, q_b=None, k_w=None,
@@ -451,6 +498,31 @@ def attn_kv4(q, k_q, k_s, v_q, v_s, k_ts, v_ts, table, lens, o, B, Lq, Hq, q_len
                                 causal, scale, ws, stream)
     if status:
         _check("attn_kv4", status)
+
+
+def attn_kv4_tree_workspace(B, Lq, Hq, H, D, max_len):
+    return lib().attn_kv4_tree_workspace(B, Lq, Hq, H, D, max_len)
+
+
+def attn_kv4_tree(q, k_q, k_s, v_q, v_s, k_ts, v_ts, table, lens, tree, o, B, Lq, Hq, q_lens=None,
+                  scale=None, ws=None, stream=None):
+    """attn_kv4 for a tree of drafted tokens: stream b's rows are the last
+    q_lens[b] of its lens[b] positions, and row t sees the positions before
+    them and the drafted tokens j with bit j % 64 of tree[b, t, j // 64] (int64
+    [B, Lq, ceil(Lq / 64)], or without the first dimension: one for all)."""
+    status = _native().attn_kv4_tree(q, k_q, k_s, v_q, v_s, k_ts, v_ts, table, lens, tree, o, B, Lq, Hq,
+                                     q_lens, scale, ws, stream)
+    if status:
+        _check("attn_kv4_tree", status)
+
+
+def kv4_keep(k_q, k_s, v_q, v_s, table, start, path, B, T, count=None, stream=None):
+    """Move the cached token at position start[b] + path[b, i] to position
+    start[b] + i, for i < count[b] (int32; None: T; path int32 [B, T]), as if all
+    were read first."""
+    status = _native().kv4_keep(k_q, k_s, v_q, v_s, table, start, path, B, T, count, stream)
+    if status:
+        _check("kv4_keep", status)
 
 
 def attn_cross_workspace(B, Lq, Lk, Hq, Hkv, D):

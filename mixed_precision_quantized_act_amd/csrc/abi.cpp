@@ -6,6 +6,7 @@
 
 #include <cmath>
 #include <new>
+#include <utility>
 #include <math.h>
 #include <stdint.h>
 
@@ -30,6 +31,8 @@ constexpr int64_t kMaxRows = (int64_t)1 << 26;  // M, N
 constexpr int64_t kMaxK = (int64_t)1 << 23;
 constexpr int64_t kMaxLd = (int64_t)1 << 32;    // row stride of heads and of a few bf16 rows
 constexpr int64_t kMaxCache = (int64_t)1 << 44; // elements of a key/value cache part
+constexpr int64_t kMaxExactK = (int64_t)1 << 17;  // |products| of 2^14 whose sums fit 32 bits
+constexpr int64_t kMaxTree = 1024;              // drafted tokens of a stream
 constexpr int64_t kMaxTiles = (int64_t)1 << 24; // 256 x 128 output tiles of one linear
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -721,12 +724,50 @@ int qlinear_bf16(const uint16_t* x, int64_t ldx, const uint8_t* w_q, const uint8
   return hip_status(launch_qgemv(x, ldx, w_q, w_s, w_ts, M, N, K, o, stream));
 }
 
+size_t qlinear_w8a8_workspace(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || check_mk(M, K) || check_nk(M, N, K) || K >= kMaxExactK) return 0;
+  return w8a8_ws_bytes(M, N, K);
+}
+
+int qlinear_w8a8(const int8_t* a_q, const float* a_s, const int8_t* w_q, const float* w_s, int64_t M,
+                 int64_t N, int64_t K, const uint16_t* bias, void* y, int64_t ldy, qa_out out,
+                 qa_epi epi, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!a_q || !a_s || !w_q || !w_s) return QA_EINVAL;
+  if (int s = check_linear(M, N, K, y, ldy, out, epi)) return s;
+  if (K >= kMaxExactK || ldy >= kMaxLd) return QA_ESHAPE;
+  if (ws_bytes && !ws) return QA_EINVAL;
+  if (!aligned16(a_q) || !aligned16(w_q) || !aligned4(a_s) || !aligned4(w_s) || !aligned16(ws) ||
+      (reinterpret_cast<uintptr_t>(bias) & 1u))
+    return QA_EALIGN;
+  const size_t ybytes = M && N ? (size_t)((M - 1) * ldy + N) * (out == QA_OUT_F32 ? 4 : 2) : 0;
+  const struct { const void* p; size_t n; } read[] = {{a_q, (size_t)(M * K)}, {a_s, (size_t)M * 4},
+                                                      {w_q, (size_t)(N * K)}, {w_s, (size_t)N * 4},
+                                                      {bias, bias ? (size_t)N * 2 : 0}};
+  for (const auto& r : read)
+    if (overlap(y, ybytes, r.p, r.n) || overlap(ws, ws_bytes, r.p, r.n)) return QA_EALIAS;
+  if (overlap(y, ybytes, ws, ws_bytes)) return QA_EALIAS;
+  if (M == 0 || N == 0) return QA_OK;
+  const GemmOut o = {y, ldy, out == QA_OUT_F32, epi == QA_EPI_GELU_TANH, bias};
+  return hip_status(launch_w8a8(a_q, a_s, w_q, w_s, M, N, K, o, ws, ws_bytes, stream));
+}
+
 // `rows` rows of H heads of D elements, of stride ld (no rows: p may be NULL)
 static int check_heads(const void* p, int64_t rows, int64_t ld, int H, int D) {
   if (H == 0) return p ? QA_EINVAL : QA_OK;
   if (!p && rows) return QA_EINVAL;
   if ((int64_t)H * D >= kMaxK || ld < (int64_t)H * D || ld % 8 || ld >= kMaxLd) return QA_ESHAPE;
   return aligned16(p) ? QA_OK : QA_EALIGN;
+}
+
+// What qk_norm_rope and qk_rope check of their outputs: each may be its input
+// itself, and no other rows of the call.
+static bool turned_rows_meet(const void* q, int64_t ldq, int64_t wq, const void* k, int64_t ldk, int64_t wk,
+                             const void* q_out, int64_t ldqo, const void* k_out, int64_t ldko, int64_t M) {
+  const bool q_in = q_out == q && ldqo == ldq, k_in = k_out == k && ldko == ldk;
+  return (!q_in && rows_overlap(q_out, ldqo, wq, q, ldq, wq, M, M)) ||
+         (!k_in && rows_overlap(k_out, ldko, wk, k, ldk, wk, M, M)) ||
+         rows_overlap(q_out, ldqo, wq, k, ldk, wk, M, M) || rows_overlap(k_out, ldko, wk, q, ldq, wq, M, M) ||
+         rows_overlap(q_out, ldqo, wq, k_out, ldko, wk, M, M);
 }
 
 int qk_norm_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int64_t ldk, int Hk,
@@ -752,13 +793,7 @@ int qk_norm_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int6
   if (!aligned16(q_w) || !aligned16(q_b) || !aligned16(k_w) || !aligned16(k_b)) return QA_EALIGN;
   if (!aligned4(cos) || !aligned4(sin) || !aligned4(pos)) return QA_EALIGN;
   const int64_t wq = (int64_t)Hq * D, wk = (int64_t)Hk * D;
-  const bool q_in = q_out == q && ldqo == ldq, k_in = k_out == k && ldko == ldk;
-  if ((!q_in && rows_overlap(q_out, ldqo, wq, q, ldq, wq, M, M)) ||
-      (!k_in && rows_overlap(k_out, ldko, wk, k, ldk, wk, M, M)) ||
-      rows_overlap(q_out, ldqo, wq, k, ldk, wk, M, M) ||
-      rows_overlap(k_out, ldko, wk, q, ldq, wq, M, M) ||
-      rows_overlap(q_out, ldqo, wq, k_out, ldko, wk, M, M))
-    return QA_EALIAS;
+  if (turned_rows_meet(q, ldq, wq, k, ldk, wk, q_out, ldqo, k_out, ldko, M)) return QA_EALIAS;
   // (positions are below 2^31)
   const int64_t table = (P < (int64_t)1 << 31 ? P : (int64_t)1 << 31) * (D / 2) * 4;
   const struct { const void* p; int64_t n; } read[] = {{q_w, D * 2}, {q_b, D * 2}, {k_w, D * 2}, {k_b, D * 2},
@@ -770,6 +805,59 @@ int qk_norm_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int6
   const QkArgs a = {q, ldq, k, ldk, M, Hq, Hk, D, norm, rope, q_w, q_b, k_w, k_b,
                     eps, 1.0f / (float)D, cos, sin, P, pos, q_out, ldqo, k_out, ldko};
   return hip_status(launch_qk_norm_rope(a, stream));
+}
+
+int qk_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int64_t ldk, int Hk, int64_t M,
+            int D, int R, qa_rope rope, const double* freq, float scale, const int32_t* pos,
+            uint16_t* q_out, int64_t ldqo, uint16_t* k_out, int64_t ldko, hipStream_t stream) {
+  if (rope != QA_ROPE_PAIRS && rope != QA_ROPE_HALVES) return QA_EINVAL;
+  if (!freq || !std::isfinite(scale)) return QA_EINVAL;
+  if (Hq < 0 || Hk < 0 || Hq + (int64_t)Hk == 0) return QA_EINVAL;
+  if (D < 16 || D > 256 || D % 16 || R < 16 || R > D || R % 16 || M < 0 || M >= (int64_t)1 << 24 ||
+      Hq + (int64_t)Hk > 65536 || M * ((int64_t)Hq + Hk) >= (int64_t)1 << 26)
+    return QA_ESHAPE;
+  if (int s = check_heads(q, M, ldq, Hq, D)) return s;
+  if (int s = check_heads(k, M, ldk, Hk, D)) return s;
+  if (int s = check_heads(q_out, M, ldqo, Hq, D)) return s;
+  if (int s = check_heads(k_out, M, ldko, Hk, D)) return s;
+  if ((reinterpret_cast<uintptr_t>(freq) & 7u) || !aligned4(pos)) return QA_EALIGN;
+  const int64_t wq = (int64_t)Hq * D, wk = (int64_t)Hk * D;
+  if (turned_rows_meet(q, ldq, wq, k, ldk, wk, q_out, ldqo, k_out, ldko, M)) return QA_EALIAS;
+  for (const auto& r : {std::pair<const void*, int64_t>{freq, R * 4}, {pos, M * 4}})
+    if (rows_meet(q_out, ldqo, wq, M, r.first, r.second) || rows_meet(k_out, ldko, wk, M, r.first, r.second))
+      return QA_EALIAS;
+  if (M == 0) return QA_OK;
+  const RopeArgs a = {q, ldq, k, ldk, M, Hq, Hk, D, R, rope, freq, scale, pos, q_out, ldqo, k_out, ldko};
+  return hip_status(launch_qk_rope(a, stream));
+}
+
+int qa_rope_freqs(qa_stretch kind, int R, double base, double factor, double original, double fast,
+                  double slow, double* freq, float* scale) {
+  if (kind < QA_STRETCH_NONE || kind > QA_STRETCH_RAMP || !freq) return QA_EINVAL;
+  if (R < 2 || R % 2 || R > 65536) return QA_ESHAPE;
+  if (!(base > 1.0) || !(factor >= 1.0) || !std::isfinite(base) || !std::isfinite(factor)) return QA_EINVAL;
+  if (kind == QA_STRETCH_BASE && R == 2) return QA_ESHAPE;
+  const bool ramp = kind == QA_STRETCH_RAMP;
+  if (ramp && !(original > 0.0 && std::isfinite(original) && slow > 0.0 && fast >= slow && std::isfinite(fast)))
+    return QA_EINVAL;
+  if (scale) *scale = ramp && factor > 1.0 ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+  const double b = kind == QA_STRETCH_BASE ? base * std::pow(factor, (double)R / (R - 2)) : base;
+  double low = 0.0, high = 0.0;
+  if (ramp) {
+    const auto at = [&](double turns) {
+      return R * std::log(original / (turns * 2.0 * 3.14159265358979323846)) / (2.0 * std::log(base));
+    };
+    low = std::fmax(std::floor(at(fast)), 0.0);
+    high = std::fmin(std::ceil(at(slow)), R - 1.0);
+    if (high - low < 0.001) high = low + 0.001;
+  }
+  for (int i = 0; i < R / 2; ++i) {
+    const double f = std::pow(b, -2.0 * i / R);
+    const double share = ramp ? std::fmin(std::fmax((i - low) / (high - low), 0.0), 1.0)
+                              : kind == QA_STRETCH_LINEAR ? 1.0 : 0.0;
+    freq[i] = f * (1.0 - share) + f / factor * share;
+  }
+  return QA_OK;
 }
 
 static int check_kv4(const Kv4Cache& c, int64_t B, int page) {
@@ -892,6 +980,25 @@ static int check_attn(const AttnArgs& a, const void* ws, size_t ws_bytes) {
   return QA_OK;
 }
 
+// what the calls over the cache check
+static int check_attn_kv4(const AttnArgs& a, const Kv4Cache& c, int page, const int32_t* lens,
+                          const int32_t* q_lens, const void* ws, size_t ws_bytes) {
+  if (!lens && a.B) return QA_EINVAL;
+  if (int s = check_kv4(c, a.B, page)) return s;
+  if (int s = check_attn(a, ws, ws_bytes)) return s;
+  if (!aligned4(lens) || !aligned4(q_lens)) return QA_EALIGN;
+  const Kv4Parts parts(c);
+  const void* outs[2] = {a.o, ws};
+  const size_t ob[2] = {rows_bytes(a.B * a.Lq, a.ldo, (int64_t)a.Hq * a.D), ws_bytes};
+  for (int i = 0; i < 2; ++i)
+    if (parts.meet(outs[i], ob[i]) || overlap(outs[i], ob[i], c.table, (size_t)(a.B * c.max_pages) * 4) ||
+        overlap(outs[i], ob[i], lens, (size_t)a.B * 4) ||
+        (q_lens && overlap(outs[i], ob[i], q_lens, (size_t)a.B * 4)) ||
+        overlap(outs[i], ob[i], c.k_ts, 4) || overlap(outs[i], ob[i], c.v_ts, 4))
+      return QA_EALIAS;
+  return QA_OK;
+}
+
 // sizes that an attention call takes, with at least one row
 static bool attn_sizes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
   return (D == 64 || D == 128) && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && B > 0 && Lq > 0 && L >= 0 &&
@@ -913,21 +1020,56 @@ int attn_kv4(const uint16_t* q, int64_t ldq, int64_t B, int64_t Lq, int Hq, int 
                       const_cast<uint8_t*>(v_q), const_cast<uint8_t*>(v_s), k_ts, v_ts, pages,
                       log2_of(page), H, D, table, max_pages};
   const AttnArgs a = {q, ldq, o, ldo, B, Lq, Hq, H, D, scale};
-  if (!lens && B) return QA_EINVAL;
-  if (int s = check_kv4(c, B, page)) return s;
-  if (int s = check_attn(a, ws, ws_bytes)) return s;
-  if (!aligned4(lens) || !aligned4(q_lens)) return QA_EALIGN;
-  const Kv4Parts parts(c);
-  const void* outs[2] = {o, ws};
-  const size_t ob[2] = {rows_bytes(B * Lq, ldo, (int64_t)Hq * D), ws_bytes};
-  for (int i = 0; i < 2; ++i)
-    if (parts.meet(outs[i], ob[i]) || overlap(outs[i], ob[i], table, (size_t)(B * max_pages) * 4) ||
-        overlap(outs[i], ob[i], lens, (size_t)B * 4) ||
-        (q_lens && overlap(outs[i], ob[i], q_lens, (size_t)B * 4)) ||
-        overlap(outs[i], ob[i], k_ts, 4) || overlap(outs[i], ob[i], v_ts, 4))
-      return QA_EALIAS;
+  if (int s = check_attn_kv4(a, c, page, lens, q_lens, ws, ws_bytes)) return s;
   if (B * Lq == 0) return QA_OK;
   return hip_status(launch_attn_kv4(a, c, lens, q_lens, causal != 0, ws, ws_bytes, stream));
+}
+
+size_t attn_kv4_tree_workspace(int64_t B, int64_t Lq, int Hq, int H, int D, int64_t max_len) {
+  return Lq <= kMaxTree ? attn_kv4_workspace(B, Lq, Hq, H, D, max_len) : 0;
+}
+
+int attn_kv4_tree(const uint16_t* q, int64_t ldq, int64_t B, int64_t Lq, int Hq, int H, int D,
+                  const uint8_t* k_q, const uint8_t* k_s, const uint8_t* v_q, const uint8_t* v_s,
+                  const float* k_ts, const float* v_ts, int64_t pages, int page,
+                  const int32_t* table, int64_t max_pages, const int32_t* lens,
+                  const int32_t* q_lens, const uint64_t* tree, int64_t tree_stride, float scale,
+                  uint16_t* o, int64_t ldo, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const Kv4Cache c = {const_cast<uint8_t*>(k_q), const_cast<uint8_t*>(k_s),
+                      const_cast<uint8_t*>(v_q), const_cast<uint8_t*>(v_s), k_ts, v_ts, pages,
+                      log2_of(page), H, D, table, max_pages};
+  const AttnArgs a = {q, ldq, o, ldo, B, Lq, Hq, H, D, scale};
+  if (!tree && B && Lq) return QA_EINVAL;
+  if (int s = check_attn_kv4(a, c, page, lens, q_lens, ws, ws_bytes)) return s;
+  const int64_t W = (Lq + 63) / 64;
+  if (Lq > kMaxTree || tree_stride < 0 || (tree_stride && tree_stride < Lq * W) || tree_stride >= kMaxLd)
+    return QA_ESHAPE;
+  if (reinterpret_cast<uintptr_t>(tree) & 7u) return QA_EALIGN;
+  if (B * Lq == 0) return QA_OK;
+  const size_t tree_bytes = (size_t)((B - 1) * tree_stride + Lq * W) * 8;
+  if (overlap(o, rows_bytes(B * Lq, ldo, (int64_t)Hq * D), tree, tree_bytes) ||
+      overlap(ws, ws_bytes, tree, tree_bytes))
+    return QA_EALIAS;
+  return hip_status(launch_attn_kv4_tree(a, c, lens, q_lens, tree, tree_stride, ws, ws_bytes, stream));
+}
+
+int kv4_keep(uint8_t* k_q, uint8_t* k_s, uint8_t* v_q, uint8_t* v_s, int64_t B, int64_t T, int H, int D,
+             int64_t pages, int page, const int32_t* table, int64_t max_pages, const int32_t* start,
+             const int32_t* path, const int32_t* count, hipStream_t stream) {
+  // (the tokens' bytes move as they are: no tensor scale is read)
+  static const float unread = 1.0f;
+  const Kv4Cache c = {k_q, k_s, v_q, v_s, &unread, &unread, pages, log2_of(page), H, D, table, max_pages};
+  if (B && T && (!start || !path)) return QA_EINVAL;
+  if (int s = check_kv4(c, B, page)) return s;
+  if (T < 0 || T > kMaxTree || B >= (int64_t)1 << 24 || B * H >= (int64_t)1 << 24) return QA_ESHAPE;
+  if (!aligned4(start) || !aligned4(path) || !aligned4(count)) return QA_EALIGN;
+  const Kv4Parts parts(c);
+  if (parts.meet_each_other() || parts.meet(table, (size_t)(B * max_pages) * 4) ||
+      parts.meet(start, (size_t)B * 4) || parts.meet(path, (size_t)(B * T) * 4) ||
+      (count && parts.meet(count, (size_t)B * 4)))
+    return QA_EALIAS;
+  if (B * T == 0) return QA_OK;
+  return hip_status(launch_kv4_keep(c, B, T, start, path, count, stream));
 }
 
 size_t attn_cross_workspace(int64_t B, int64_t Lq, int64_t Lk, int Hq, int Hkv, int D) {

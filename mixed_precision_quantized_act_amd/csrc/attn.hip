@@ -1,5 +1,5 @@
-// Attention of bf16 queries over an NVFP4 cache (attn_kv4) and over an
-// encoder's bf16 states (attn_cross):
+// Attention of bf16 queries over an NVFP4 cache (attn_kv4; attn_kv4_tree: of a
+// tree of drafted tokens) and over an encoder's bf16 states (attn_cross):
 //
 //   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale (q . k_j) - max)
 //
@@ -40,6 +40,13 @@ hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4Cache& c, const int32_t* 
                            hipStream_t stream) {
   return launch(a, Kv4Source{c, lens, q_lens, causal ? 1 : 0}, c.max_pages << c.page_log2, ws,
                 ws_bytes, stream);
+}
+
+hipError_t launch_attn_kv4_tree(const AttnArgs& a, const Kv4Cache& c, const int32_t* lens,
+                                const int32_t* q_lens, const uint64_t* tree, int64_t stride, void* ws,
+                                size_t ws_bytes, hipStream_t stream) {
+  const Kv4TreeSource src = {{c, lens, q_lens, 0}, tree, stride, (int)((a.Lq + 63) / 64)};
+  return launch(a, src, c.max_pages << c.page_log2, ws, ws_bytes, stream);
 }
 
 hipError_t launch_attn_cross(const AttnArgs& a, const uint16_t* k, int64_t ldk, const uint16_t* v,

@@ -139,7 +139,7 @@ struct Kv4Source {
   const int32_t* q_lens;
   int causal;
 
-  static constexpr bool kF16 = true;
+  static constexpr bool kF16 = true, kTree = false;
   __device__ int queries(int64_t b, int64_t Lq) const {
     if (!q_lens) return (int)Lq;
     const int n = q_lens[b];
@@ -189,6 +189,27 @@ struct Kv4Source {
   __device__ float v_scale() const { return *c.v_ts; }
 };
 
+// The same where the last keys of a stream are the query rows' own tokens, a tree
+// of drafted ones: row t sees every key before them and of them those whose bits
+// its words name.
+struct Kv4TreeSource : Kv4Source {
+  const uint64_t* tree;            // [Lq][words], `stride` words apart for the streams
+  int64_t stride;
+  int words;
+
+  static constexpr bool kTree = true;
+  // Bit j: row t sees key base + j; own: the first of the rows' own keys.  (Bits
+  // behind the last key are of any value.)
+  __device__ __forceinline__ uint64_t row_sees(const uint64_t* row, int base, int own) const {
+    const int rel = base - own;                      // of key base among the own ones
+    if (rel <= -64) return ~0ull;
+    if (rel < 0) return ~0ull >> (64 + rel) | row[0] << -rel;
+    const int w = rel >> 6, at = rel & 63;
+    const uint64_t lo = w < words ? row[w] >> at : 0;
+    return at && w + 1 < words ? lo | row[w + 1] << (64 - at) : lo;
+  }
+};
+
 // Keys and values of an encoder (bf16 operands).
 struct CrossSource {
   const uint16_t* k;
@@ -198,7 +219,7 @@ struct CrossSource {
   const int32_t* k_lens;
   const uint8_t* mask;
 
-  static constexpr bool kF16 = false;
+  static constexpr bool kF16 = false, kTree = false;
   // The mask's byte for state base + lane.
   struct Look {
     uint32_t on;

@@ -43,6 +43,8 @@ __device__ __forceinline__ T fetch(const void* p) {
 
 template <class Source, int D, bool Once>
 struct Few;
+template <int D, bool Once>
+struct Few<Kv4TreeSource, D, Once> : Few<Kv4Source, D, Once> {};
 
 // NVFP4: per 64 keys a lane holds for each of four 16-key tiles the codes of
 // D/4 elements of key (lane & 15) and their group scales, V's codes as they lie
@@ -279,7 +281,7 @@ attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gat
 
   // keys that this lane's row sees, and that every row of the tile sees
   const int upto = src.causal ? n - (nq - 1 - t) : n;
-  const int all = src.causal ? n - (nq - 1 - row0 / G) : n;
+  const int all = Source::kTree ? n - nq : src.causal ? n - (nq - 1 - row0 / G) : n;
   const int last = min(row0 + kFewRows, rows) - 1;
   const int end = src.causal ? n - (nq - 1 - last / G) : n;       // that any row sees
   const int chunks = (max(end, 0) + kFewKeys - 1) / kFewKeys;
@@ -301,6 +303,9 @@ attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gat
 #pragma unroll
   for (int d = 0; d < D / 16; ++d) o[d] = f32x4{0, 0, 0, 0};
   float m = -INFINITY, l = 0.0f;                 // m: largest product, before the scale
+
+  const uint64_t* words = nullptr;               // a tree's, of this lane's row
+  if constexpr (Source::kTree) words = src.tree + b * src.stride + (int64_t)min(t, nq - 1) * src.words;
 
   typename F::Regs cur;
   typename Source::Look look = {};
@@ -329,12 +334,14 @@ attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gat
     }
     const bool whole = seen == ~0ull && base + kFewKeys <= all;
     if (!whole) {
+      uint64_t mine = seen;
+      if constexpr (Source::kTree) mine &= src.row_sees(words, base, all);
 #pragma unroll
       for (int t4 = 0; t4 < 4; ++t4)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int key = 16 * t4 + 4 * g + r;
-          const bool on = ((seen >> key) & 1) && base + key < upto;
+          const bool on = ((mine >> key) & 1) && base + key < upto;
           s[t4][r] = on ? s[t4][r] : -INFINITY;
         }
     }
@@ -561,6 +568,10 @@ template hipError_t launch_attn_join(const AttnArgs&, const Kv4Source&, const At
 template hipError_t launch_attn_join(const AttnArgs&, const CrossSource&, const AttnSplit&, int,
                                      hipStream_t);
 template hipError_t launch_attn_few(const AttnArgs&, const Kv4Source&, int64_t, void*, size_t,
+                                    hipStream_t);
+template hipError_t launch_attn_join(const AttnArgs&, const Kv4TreeSource&, const AttnSplit&, int,
+                                     hipStream_t);
+template hipError_t launch_attn_few(const AttnArgs&, const Kv4TreeSource&, int64_t, void*, size_t,
                                     hipStream_t);
 template hipError_t launch_attn_few(const AttnArgs&, const CrossSource&, int64_t, void*, size_t,
                                     hipStream_t);

@@ -101,6 +101,54 @@ kv4_read_kernel(Kv4Cache c, uint16_t* __restrict__ k, int64_t ldk, uint16_t* __r
   }
 }
 
+// The kept tokens of a stream: a workgroup takes one key head's keys or values,
+// `cols` groups of 16 elements of every token, a group per lane and turn, and
+// holds them all in registers before it writes the first, so that sources and
+// places may be the same slots in any order.
+constexpr int kKeepTurns = 8;
+
+__global__ void __launch_bounds__(256)
+kv4_keep_kernel(Kv4Cache c, int T, int cols, const int32_t* __restrict__ start,
+                const int32_t* __restrict__ path, const int32_t* __restrict__ count, Gate gate) {
+  if (gated_off(gate)) return;
+  const int64_t b = blockIdx.x / (uint32_t)c.H;
+  const int head = (int)(blockIdx.x - (uint32_t)b * c.H);
+  const bool val = blockIdx.z != 0;
+  uint8_t* const q = val ? c.v_q : c.k_q;
+  uint8_t* const s = val ? c.v_s : c.k_s;
+  const int n = count ? min(count[b], T) : T;
+  const int64_t first = start[b];
+  const int col0 = blockIdx.y * cols, width = min(cols, c.D / 16 - col0);
+  u32x2 w[kKeepTurns];
+  uint32_t sc[kKeepTurns];
+  int64_t to[kKeepTurns];
+#pragma unroll
+  for (int u = 0; u < kKeepTurns; ++u) {
+    const int x = u * 256 + threadIdx.x, i = x / width, col = col0 + (x - i * width);
+    w[u] = u32x2{0, 0};
+    sc[u] = 0;
+    to[u] = -1;
+    if (i >= n) continue;
+    const int64_t src = kv4_slot(c, b, first + path[b * T + i], head);
+    const int64_t dst = kv4_slot(c, b, first + i, head);
+    if (src < 0 || dst < 0 || src == dst) continue;
+    w[u] = *reinterpret_cast<const u32x2*>(q + src * (c.D / 2) + 8 * col);
+    sc[u] = s[src * (c.D / 16) + col];
+    to[u] = dst;
+  }
+  // (in their registers before any wave of the workgroup stores)
+#pragma unroll
+  for (int u = 0; u < kKeepTurns; ++u) asm volatile("" : "+v"(w[u]), "+v"(sc[u]));
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kKeepTurns; ++u) {
+    if (to[u] < 0) continue;
+    const int x = u * 256 + threadIdx.x, col = col0 + x % width;
+    *reinterpret_cast<u32x2*>(q + to[u] * (c.D / 2) + 8 * col) = w[u];
+    s[to[u] * (c.D / 16) + col] = (uint8_t)sc[u];
+  }
+}
+
 }  // namespace
 
 hipError_t launch_kv4_append(const Kv4Cache& c, const uint16_t* k, int64_t ldk, const uint16_t* v,
@@ -122,6 +170,15 @@ hipError_t launch_kv4_read(const Kv4Cache& c, uint16_t* k, int64_t ldk, uint16_t
   hipLaunchKernelGGL(kv4_read_kernel, grid, dim3(256), 0, stream, c, k, ldk, v, ldv,
                      (uint32_t)T, groups,
                      start, count, current_gate());
+  return hipGetLastError();
+}
+
+hipError_t launch_kv4_keep(const Kv4Cache& c, int64_t B, int64_t T, const int32_t* start,
+                           const int32_t* path, const int32_t* count, hipStream_t stream) {
+  const int groups = c.D / 16, fit = (int)(256 * kKeepTurns / T), cols = fit < groups ? fit : groups;
+  const dim3 grid((unsigned)(B * c.H), (unsigned)((groups + cols - 1) / cols), 2);
+  hipLaunchKernelGGL(kv4_keep_kernel, grid, dim3(256), 0, stream, c, (int)T, cols, start, path, count,
+                     current_gate());
   return hipGetLastError();
 }
 

@@ -28,6 +28,10 @@ decltype(&kv4_append) f_kv4_append;
 decltype(&kv4_read) f_kv4_read;
 decltype(&attn_kv4) f_attn_kv4;
 decltype(&attn_cross) f_attn_cross;
+decltype(&qlinear_w8a8) f_qlinear_w8a8;
+decltype(&qk_rope) f_qk_rope;
+decltype(&attn_kv4_tree) f_attn_kv4_tree;
+decltype(&kv4_keep) f_kv4_keep;
 
 // A refused argument; ends at the module's functions.
 [[noreturn]] void refuse(const char* format, ...) {
@@ -125,12 +129,12 @@ int64_t rows(const Tensor& t, int64_t n, int64_t width, const char* name, int64_
 
 // The same for a stride that the caller gives (None: the tensor's own): the
 // last row has to end within the tensor's storage, whatever its shape.  (More
-// rows than the library takes, or smaller strides, it refuses itself.)
+// rows than the library takes, `most`, or smaller strides, it refuses itself.)
 int64_t rows_of(PyObject* given, const Tensor& t, int64_t n, int64_t width, const char* name,
-                int64_t step = 8) {
+                int64_t step = 8, int64_t most = QA_ROWS_MAX) {
   if (given == Py_None) return rows(t, n, width, name, step);
   const int64_t ld = integer(given), item = (int64_t)t.itemsize();
-  if (n < 1 || n > QA_ROWS_MAX || width < 1 || ld < width) return ld;
+  if (n < 1 || n > most || width < 1 || ld < width) return ld;
   const int64_t has = (int64_t)t.storage().nbytes() / item - t.storage_offset();
   if (width > has || (n > 1 && ld > (has - width) / (n - 1)))
     refuse("%s: %lld rows of %lld elements, %lld apart, do not fit the %lld that it has", name,
@@ -138,25 +142,26 @@ int64_t rows_of(PyObject* given, const Tensor& t, int64_t n, int64_t width, cons
   return ld;
 }
 
-// The parts of an NVFP4 cache and its table: 7 arguments.
+// The parts of an NVFP4 cache and its table: 7 arguments, or 5 without the tensor
+// scales.
 struct Cache {
   uint8_t* part[4];
   const float *k_ts, *v_ts;
   const int32_t* table;
   int64_t pages, max_pages;
   int H, page, D;
-  Cache(const Place& p, PyObject* const* a, int64_t B) {
+  Cache(const Place& p, PyObject* const* a, int64_t B, bool scaled = true) {
     static const char* const kNames[4] = {"k_q", "k_s", "v_q", "v_s"};
     const Tensor* t[4];
     for (int i = 0; i < 4; ++i) {
       t[i] = &needed(tensor(p, a[i], kNames[i], at::kByte, kWhole), kNames[i]);
       part[i] = ptr<uint8_t>(t[i]);
     }
-    const Tensor& ks = needed(tensor(p, a[4], "k_ts", at::kFloat), "k_ts");
-    const Tensor& vs = needed(tensor(p, a[5], "v_ts", at::kFloat), "v_ts");
-    const Tensor& tb = needed(tensor(p, a[6], "table", at::kInt, kWhole), "table");
-    sized(&ks, 1, "k_ts");
-    sized(&vs, 1, "v_ts");
+    const Tensor* ks = scaled ? &needed(tensor(p, a[4], "k_ts", at::kFloat), "k_ts") : nullptr;
+    const Tensor* vs = scaled ? &needed(tensor(p, a[5], "v_ts", at::kFloat), "v_ts") : nullptr;
+    const Tensor& tb = needed(tensor(p, a[scaled ? 6 : 4], "table", at::kInt, kWhole), "table");
+    sized(ks, 1, "k_ts");
+    sized(vs, 1, "v_ts");
     if (t[0]->dim() != 4 || tb.dim() != 2)
       refuse("a cache part is [pages, H, page, D / 2], a table [B, max_pages]");
     const at::IntArrayRef q = t[0]->sizes();
@@ -168,8 +173,8 @@ struct Cache {
       refuse("table: needs %lld rows, got %lld", (long long)B, (long long)tb.size(0));
     if (q[1] > INT32_MAX || q[2] > INT32_MAX || q[3] > INT32_MAX / 2)
       refuse("the cache parts' shapes are too large");
-    k_ts = ptr<float>(&ks);
-    v_ts = ptr<float>(&vs);
+    k_ts = ptr<float>(ks);
+    v_ts = ptr<float>(vs);
     table = ptr<int32_t>(&tb);
     pages = q[0];
     H = (int)q[1];
@@ -361,7 +366,114 @@ PyObject* py_attn_cross(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// The addresses of the six functions, in the order above.
+// a_q, a_s, w_q, w_s, y, M, N, K, bias, out, epi, ldy, ws, stream
+PyObject* py_qlinear_w8a8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 14, [&] {
+    const Place p(a[13]);
+    const int64_t M = integer(a[5]), N = integer(a[6]), K = integer(a[7]);
+    const int out = small(a[9], "out"), epi = small(a[10], "epi");
+    const Tensor* aq = tensor(p, a[0], "a_q", at::kChar, kWhole);
+    const Tensor* as = tensor(p, a[1], "a_s", at::kFloat, kWhole);
+    const Tensor* wq = tensor(p, a[2], "w_q", at::kChar, kWhole);
+    const Tensor* wsc = tensor(p, a[3], "w_s", at::kFloat, kWhole);
+    const Tensor& y = needed(tensor(p, a[4], "y", out == QA_OUT_F32 ? at::kFloat : at::kBFloat16), "y");
+    const Tensor* bias = tensor(p, a[8], "bias", at::kBFloat16, kWhole);
+    const Tensor* ws = tensor(p, a[12], "ws", at::kByte, kWhole);
+    if (K > 0 && K < (int64_t)1 << 23) {
+      if (M > 0 && M < (int64_t)1 << 26) sized(aq, M * K, "a_q");
+      if (N > 0 && N < (int64_t)1 << 26) sized(wq, N * K, "w_q");
+    }
+    sized(as, M, "a_s");
+    sized(wsc, N, "w_s");
+    sized(bias, N, "bias");
+    const int64_t ldy = rows_of(a[11], y, M, N, "y", 1, (int64_t)1 << 26);
+    return run([&] {
+      return f_qlinear_w8a8(place<int8_t>(aq), place<float>(as), place<int8_t>(wq), place<float>(wsc), M, N, K,
+                            ptr<uint16_t>(bias), place<void>(&y), ldy, (qa_out)out, (qa_epi)epi,
+                            ptr<void>(ws), ws ? (size_t)ws->numel() : 0, p.stream);
+    });
+  });
+}
+
+// q, k, q_out, k_out, M, Hq, Hk, D, R, freq, rope, scale, pos, stream
+PyObject* py_qk_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 14, [&] {
+    const Place p(a[13]);
+    static const char* const kNames[4] = {"q", "k", "q_out", "k_out"};
+    const int64_t M = integer(a[4]);
+    const int H[2] = {small(a[5], "Hq"), small(a[6], "Hk")}, D = small(a[7], "D"), R = small(a[8], "R");
+    const Tensor* t[4];
+    int64_t ld[4] = {0, 0, 0, 0};
+    for (int i = 0; i < 4; ++i) {
+      t[i] = tensor(p, a[i], kNames[i], at::kBFloat16);
+      if (t[i]) ld[i] = rows(*t[i], M, (int64_t)H[i & 1] * D, kNames[i]);
+    }
+    const Tensor& freq = needed(tensor(p, a[9], "freq", at::kDouble, kWhole), "freq");
+    const Tensor* pos = tensor(p, a[12], "pos", at::kInt, kWhole);
+    sized(&freq, R / 2, "freq");
+    sized(pos, M, "pos");
+    const int rope = small(a[10], "rope");
+    const float scale = (float)real(a[11]);
+    return run([&] {
+      return f_qk_rope(ptr<uint16_t>(t[0]), ld[0], H[0], ptr<uint16_t>(t[1]), ld[1], H[1], M, D, R,
+                       (qa_rope)rope, ptr<double>(&freq), scale, ptr<int32_t>(pos), ptr<uint16_t>(t[2]),
+                       ld[2], ptr<uint16_t>(t[3]), ld[3], p.stream);
+    });
+  });
+}
+
+// q, the cache (7), lens, tree, o, B, Lq, Hq, q_lens, scale, ws, stream
+PyObject* py_attn_kv4_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 18, [&] {
+    const Place p(a[17]);
+    const int64_t B = integer(a[11]), Lq = integer(a[12]);
+    const int Hq = small(a[13], "Hq");
+    const Cache c(p, a + 1, B);
+    const Tensor& q = needed(tensor(p, a[0], "q", at::kBFloat16), "q");
+    const Tensor* lens = tensor(p, a[8], "lens", at::kInt, kWhole);
+    const Tensor& tree = needed(tensor(p, a[9], "tree", at::kLong, kWhole), "tree");
+    const Tensor& o = needed(tensor(p, a[10], "o", at::kBFloat16), "o");
+    const Tensor* q_lens = tensor(p, a[14], "q_lens", at::kInt, kWhole);
+    const Tensor* ws = tensor(p, a[16], "ws", at::kByte, kWhole);
+    sized(lens, B, "lens");
+    sized(q_lens, B, "q_lens");
+    const int64_t W = Lq / 64 + (Lq % 64 != 0), dims = tree.dim();
+    if ((dims != 2 && dims != 3) || tree.size(-2) != Lq || tree.size(-1) != W || (dims == 3 && tree.size(0) < B))
+      refuse("tree: needs shape [%lld, %lld, %lld], or [%lld, %lld] for all streams", (long long)B,
+             (long long)Lq, (long long)W, (long long)Lq, (long long)W);
+    const float scale = scale_of(a[15], c.D);
+    const int64_t w = (int64_t)Hq * c.D, ldq = rows(q, product(B, Lq), w, "q");
+    const int64_t ldo = rows(o, product(B, Lq), w, "o");
+    return run([&] {
+      return f_attn_kv4_tree(ptr<uint16_t>(&q), ldq, B, Lq, Hq, c.H, c.D, c.part[0], c.part[1], c.part[2],
+                             c.part[3], c.k_ts, c.v_ts, c.pages, c.page, c.table, c.max_pages,
+                             ptr<int32_t>(lens), ptr<int32_t>(q_lens), ptr<uint64_t>(&tree),
+                             dims == 3 ? Lq * W : 0, scale, ptr<uint16_t>(&o), ldo, ptr<void>(ws),
+                             ws ? (size_t)ws->numel() : 0, p.stream);
+    });
+  });
+}
+
+// the cache without its scales (5), start, path, B, T, count, stream
+PyObject* py_kv4_keep(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&] {
+    const Place p(a[10]);
+    const int64_t B = integer(a[7]), T = integer(a[8]);
+    const Cache c(p, a, B, false);
+    const Tensor* start = tensor(p, a[5], "start", at::kInt, kWhole);
+    const Tensor* path = tensor(p, a[6], "path", at::kInt, kWhole);
+    const Tensor* count = tensor(p, a[9], "count", at::kInt, kWhole);
+    sized(start, B, "start");
+    sized(path, product(B, T), "path");
+    sized(count, B, "count");
+    return run([&] {
+      return f_kv4_keep(c.part[0], c.part[1], c.part[2], c.part[3], B, T, c.H, c.D, c.pages, c.page, c.table,
+                        c.max_pages, ptr<int32_t>(start), ptr<int32_t>(path), ptr<int32_t>(count), p.stream);
+    });
+  });
+}
+
+// The addresses of the first six functions, in the order above.
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 6, [&]() -> PyObject* {
     uintptr_t at[6];
@@ -376,11 +488,26 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// and of the four after them
+PyObject* py_bind_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 4, [&]() -> PyObject* {
+    uintptr_t at[4];
+    for (int i = 0; i < 4; ++i) at[i] = (uintptr_t)integer(a[i]);
+    f_qlinear_w8a8 = reinterpret_cast<decltype(f_qlinear_w8a8)>(at[0]);
+    f_qk_rope = reinterpret_cast<decltype(f_qk_rope)>(at[1]);
+    f_attn_kv4_tree = reinterpret_cast<decltype(f_attn_kv4_tree)>(at[2]);
+    f_kv4_keep = reinterpret_cast<decltype(f_kv4_keep)>(at[3]);
+    Py_RETURN_NONE;
+  });
+}
+
 #define QACT_METHOD(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_##name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {QACT_METHOD(bind),       QACT_METHOD(qlinear_bf16), QACT_METHOD(qk_norm_rope),
                           QACT_METHOD(kv4_append), QACT_METHOD(kv4_read),     QACT_METHOD(attn_kv4),
-                          QACT_METHOD(attn_cross), {nullptr, nullptr, 0, nullptr}};
+                          QACT_METHOD(attn_cross), QACT_METHOD(bind_step),    QACT_METHOD(qlinear_w8a8),
+                          QACT_METHOD(qk_rope),    QACT_METHOD(attn_kv4_tree), QACT_METHOD(kv4_keep),
+                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_call", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -153,6 +153,29 @@ hipError_t launch_qgemv(const uint16_t* x, int64_t ldx, const uint8_t* w_q, cons
                         const float* w_ts, int64_t M, int64_t N, int64_t K, const GemmOut& o,
                         hipStream_t stream);
 
+// ---- INT8 activations against an INT8 weight (qgemm_w8a8.hip)
+size_t w8a8_ws_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_w8a8(const int8_t* a_q, const float* a_s, const int8_t* w_q, const float* w_s, int64_t M,
+                       int64_t N, int64_t K, const GemmOut& o, void* ws, size_t ws_bytes, hipStream_t st);
+
+// ---- rotation of query and key heads by their positions (qk_rope.hip)
+struct RopeArgs {
+  const uint16_t* q;
+  int64_t ldq;
+  const uint16_t* k;
+  int64_t ldk, M;
+  int Hq, Hk, D, R;
+  int rope;               // qa_rope
+  const double* freq;
+  float scale;
+  const int32_t* pos;
+  uint16_t* q_out;
+  int64_t ldqo;
+  uint16_t* k_out;
+  int64_t ldko;
+};
+hipError_t launch_qk_rope(const RopeArgs& a, hipStream_t stream);
+
 // ---- norm and rotation of query and key heads (qk_norm.hip)
 struct QkArgs {
   const uint16_t* q;
@@ -190,6 +213,10 @@ hipError_t launch_kv4_read(const Kv4Cache& c, uint16_t* k, int64_t ldk, uint16_t
                            int64_t B, int64_t T, const int32_t* start, const int32_t* count,
                            hipStream_t stream);
 
+// tokens start + path[i] of each stream to start + i, i < count (kv4.hip)
+hipError_t launch_kv4_keep(const Kv4Cache& c, int64_t B, int64_t T, const int32_t* start,
+                           const int32_t* path, const int32_t* count, hipStream_t stream);
+
 // ---- attention (attn.hip)
 struct AttnArgs {
   const uint16_t* q;
@@ -206,6 +233,10 @@ size_t attn_cross_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_
 hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4Cache& c, const int32_t* lens,
                            const int32_t* q_lens, bool causal, void* ws, size_t ws_bytes,
                            hipStream_t stream);
+// tree: words of each row's drafted tokens, `stride` apart for the streams
+hipError_t launch_attn_kv4_tree(const AttnArgs& a, const Kv4Cache& c, const int32_t* lens,
+                                const int32_t* q_lens, const uint64_t* tree, int64_t stride, void* ws,
+                                size_t ws_bytes, hipStream_t stream);
 hipError_t launch_attn_cross(const AttnArgs& a, const uint16_t* k, int64_t ldk, const uint16_t* v,
                              int64_t ldv, int64_t Lk, const int32_t* k_lens, const uint8_t* mask,
                              void* ws, size_t ws_bytes, hipStream_t stream);
