@@ -23,7 +23,7 @@ ROOT = os.path.dirname(HERE)
 OBJ_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["act_quant.hip", "qgemm.hip", "qgemm_i8.hip", "tdc.hip", "noalloc.hip", "convert_check.hip", "stage_ab.hip",
-           "qgemv.hip", "qgemm_w8a8.hip", "qk_norm.hip", "qk_rope.hip", "kv4.hip", "attn.hip", "attn_few.hip",
+           "qgemv.hip", "qgemm_w8a8.hip", "w8a8_split.hip", "qk_norm.hip", "qk_rope.hip", "kv4.hip", "attn.hip", "attn_few.hip",
            "attn_tile.hip", "attn_short.hip", "abi.cpp"]
 
 FLAGS = [
