@@ -1026,7 +1026,7 @@ int attn_kv4(const uint16_t* q, int64_t ldq, int64_t B, int64_t Lq, int Hq, int 
 }
 
 size_t attn_kv4_tree_workspace(int64_t B, int64_t Lq, int Hq, int H, int D, int64_t max_len) {
-  return Lq <= kMaxTree ? attn_kv4_workspace(B, Lq, Hq, H, D, max_len) : 0;
+  return Lq <= kMaxTree && attn_sizes(B, Lq, Hq, H, D, max_len) ? attn_kv4_tree_ws_bytes(B, Lq, Hq, H, D, max_len) : 0;
 }
 
 int attn_kv4_tree(const uint16_t* q, int64_t ldq, int64_t B, int64_t Lq, int Hq, int H, int D,

@@ -42,11 +42,25 @@ hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4Cache& c, const int32_t* 
                 ws_bytes, stream);
 }
 
+namespace {
+
+// Rows of a key head up to which a tree's are taken in halves of 128.
+bool halves(int64_t Lq, int Hq, int Hkv) { return Lq * (Hq / Hkv) <= 128; }
+
+}  // namespace
+
+size_t attn_kv4_tree_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
+  if (many(Lq, Hq, Hkv) && halves(Lq, Hq, Hkv)) return attn_tree_ws_bytes(B, Lq, Hq, Hkv, D, L);
+  return attn_ws_bytes(B, Lq, Hq, Hkv, D, L);
+}
+
 hipError_t launch_attn_kv4_tree(const AttnArgs& a, const Kv4Cache& c, const int32_t* lens,
                                 const int32_t* q_lens, const uint64_t* tree, int64_t stride, void* ws,
                                 size_t ws_bytes, hipStream_t stream) {
   const Kv4TreeSource src = {{c, lens, q_lens, 0}, tree, stride, (int)((a.Lq + 63) / 64)};
-  return launch(a, src, c.max_pages << c.page_log2, ws, ws_bytes, stream);
+  const int64_t L = c.max_pages << c.page_log2;
+  if (many(a.Lq, a.Hq, a.Hkv) && halves(a.Lq, a.Hq, a.Hkv)) return launch_attn_tree(a, src, L, ws, ws_bytes, stream);
+  return launch(a, src, L, ws, ws_bytes, stream);
 }
 
 hipError_t launch_attn_cross(const AttnArgs& a, const uint16_t* k, int64_t ldk, const uint16_t* v,
