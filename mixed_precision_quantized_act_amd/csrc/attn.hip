@@ -44,14 +44,23 @@ hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4Cache& c, const int32_t* 
 
 namespace {
 
-// Rows of a key head up to which a tree's are taken in halves of 128.
-bool halves(int64_t Lq, int Hq, int Hkv) { return Lq * (Hq / Hkv) <= 128; }
+// Which kernel takes a tree.  The few rows' (16 or 32 a wave, by itself) up to 48
+// rows of a key head, and where a SIMD has at most 6 of its steps of 16 rows and 64 keys
+// (the start of the tiles of many rows takes as long: 64 rows, 8 key heads of
+// 128, 4000 keys: 14.3 us, by the tiles 19.0; 128 rows, 32 key heads, 1000 keys: 22.5 and
+// 24.7; 4000 keys: 37.8 and 31.6).  Above, tiles of 128 or 256 rows, but up to 64 rows,
+// half a tile, only below 64 steps a SIMD (128 key heads, 4000 keys: 49.7 us and
+// 53.7 by the few rows'; 32768 keys: 285 and 212).
+bool tree_few(int64_t B, int64_t Lq, int Hq, int Hkv, int64_t L) {
+  const int64_t rows = Lq * (Hq / Hkv), steps = B * Hkv * ((rows + 15) / 16) * ((L + 63) / 64);
+  return rows <= 48 || steps <= 6 * 1024 || (rows <= 64 && steps >= 64 * 1024);
+}
 
 }  // namespace
 
 size_t attn_kv4_tree_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
-  if (many(Lq, Hq, Hkv) && halves(Lq, Hq, Hkv)) return attn_tree_ws_bytes(B, Lq, Hq, Hkv, D, L);
-  return attn_ws_bytes(B, Lq, Hq, Hkv, D, L);
+  return tree_few(B, Lq, Hq, Hkv, L) ? attn_few_ws_bytes(B, Lq, Hq, Hkv, D, L)
+                                     : attn_tree_ws_bytes(B, Lq, Hq, Hkv, D, L);
 }
 
 hipError_t launch_attn_kv4_tree(const AttnArgs& a, const Kv4Cache& c, const int32_t* lens,
@@ -59,8 +68,8 @@ hipError_t launch_attn_kv4_tree(const AttnArgs& a, const Kv4Cache& c, const int3
                                 size_t ws_bytes, hipStream_t stream) {
   const Kv4TreeSource src = {{c, lens, q_lens, 0}, tree, stride, (int)((a.Lq + 63) / 64)};
   const int64_t L = c.max_pages << c.page_log2;
-  if (many(a.Lq, a.Hq, a.Hkv) && halves(a.Lq, a.Hq, a.Hkv)) return launch_attn_tree(a, src, L, ws, ws_bytes, stream);
-  return launch(a, src, L, ws, ws_bytes, stream);
+  if (tree_few(a.B, a.Lq, a.Hq, a.Hkv, L)) return launch_attn_few(a, src, L, ws, ws_bytes, stream);
+  return launch_attn_tree(a, src, L, ws, ws_bytes, stream);
 }
 
 hipError_t launch_attn_cross(const AttnArgs& a, const uint16_t* k, int64_t ldk, const uint16_t* v,

@@ -18,6 +18,8 @@
 // 16 streams of 16384 to 32768 tokens, one query token each, 32 query and 8 key
 // heads of 128: 92 us and 4.7 for the join in a kernel trace, 463 MB at 5.0 TB/s.  24
 // tokens to 300 to 1500 bf16 states, 20 heads of 64: 25 us and 4.8.
+#include <type_traits>
+
 #include "attn_common.h"
 
 namespace qact {
@@ -142,6 +144,9 @@ struct Few<Kv4Source, D, Once> {
   static __device__ __forceinline__ int swizzle(int key) {
     return D == 128 ? (key >> 2) & 3 : (key >> 3) & 1;
   }
+  // Tree: a drafted token that some rows do not see may have a NaN's scale, and its
+  // weight of zero needs a number (act_quant's are at most 448).
+  template <bool Tree>
   static __device__ __forceinline__ void stage_v(const Regs& r, char* lds, int lane) {
 #pragma unroll
     for (int u = 0; u < kVLoads; ++u) {
@@ -152,8 +157,14 @@ struct Few<Kv4Source, D, Once> {
     const bool on = (r.seen >> lane) & 1;      // (bytes of slots that are not seen may be NaN codes)
 #pragma unroll
     for (int i = 0; i < kGroups / 4; ++i) {
-      const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)r.vs[i], false);
-      const f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8((int)r.vs[i], true);
+      f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)r.vs[i], false);
+      f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8((int)r.vs[i], true);
+      if constexpr (Tree)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          a[j] = fminf(a[j], 448.0f);
+          b[j] = fminf(b[j], 448.0f);
+        }
       sc[(4 * i + 0) * kFewKeys + lane] = (_Float16)(on ? a[0] : 0.0f);
       sc[(4 * i + 1) * kFewKeys + lane] = (_Float16)(on ? a[1] : 0.0f);
       sc[(4 * i + 2) * kFewKeys + lane] = (_Float16)(on ? b[0] : 0.0f);
@@ -226,6 +237,7 @@ struct Few<CrossSource, D, Once> {
   static __device__ __forceinline__ int swizzle(int key) {
     return D == 128 ? key & 7 : (key >> 1) & 3;
   }
+  template <bool>
   static __device__ __forceinline__ void stage_v(const Regs& r, char* lds, int lane) {
 #pragma unroll
     for (int u = 0; u < kVLoads; ++u) {
@@ -252,17 +264,19 @@ struct Few<CrossSource, D, Once> {
 // Workgroup: (stream, key head, row tile, split), the split running fastest.
 // (Two waves per SIMD keep the compiler from spending more registers than help, 105
 // -> 102 us for 16 streams; bf16 of 128 would spill, 54 -> 75 us.)
-template <class Source, int D, bool Once>
+// A wave takes `Sets` times 16 rows, for which a key's codes become numbers once.
+template <class Source, int D, bool Once, int Sets>
 __global__ void __launch_bounds__(64 * kFewWaves, !Source::kF16 && D == 128 ? 1 : 2)
 attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gate gate) {
   if (gated_off(gate)) return;
   using F = Few<Source, D, Once>;
   constexpr bool kF16 = Source::kF16;
-  constexpr int kJoin = kFewWaves * kFewRows * (D + 4) * 4;       // the waves' sums
+  constexpr int kRows = Sets * kFewRows;
+  constexpr int kJoin = kFewWaves * kRows * (D + 4) * 4;          // the waves' sums
   constexpr int kLds = kFewWaves * F::kLds > kJoin ? kFewWaves * F::kLds : kJoin;
   __shared__ __align__(16) char lds[kLds];
-  __shared__ float ml[2][kFewWaves][kFewRows];      // each wave's maximum and sum of a row
-  __shared__ float fin[2][kFewRows];                // the row's
+  __shared__ float ml[2][kFewWaves][kRows];         // each wave's maximum and sum of a row
+  __shared__ float fin[2][kRows];                   // the row's
 
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -273,39 +287,47 @@ attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gat
   const int G = a.Hq / a.Hkv;
   const int nq = src.queries(b, a.Lq), n = src.keys(b);
   const int rows = nq * G;
-  const int row0 = tile * kFewRows;
+  const int row0 = tile * kRows;
   if (row0 >= rows) return;
-  const int row = row0 + col, t = row / G;
-  const int64_t qrow = b * a.Lq + t;
-  const int head = hk * G + (row - t * G);
 
-  // keys that this lane's row sees, and that every row of the tile sees
-  const int upto = src.causal ? n - (nq - 1 - t) : n;
+  // keys that every row of the tile sees, and that any does
   const int all = Source::kTree ? n - nq : src.causal ? n - (nq - 1 - row0 / G) : n;
-  const int last = min(row0 + kFewRows, rows) - 1;
-  const int end = src.causal ? n - (nq - 1 - last / G) : n;       // that any row sees
+  const int last = min(row0 + kRows, rows) - 1;
+  const int end = src.causal ? n - (nq - 1 - last / G) : n;
   const int chunks = (max(end, 0) + kFewKeys - 1) / kFewKeys;
   const int c0 = (int)((int64_t)chunks * split / splits);
   const int c1 = (int)((int64_t)chunks * (split + 1) / splits);
 
-  u32x4 q[D / 32];
+  int upto[Sets];                                // keys that this lane's rows see
+  const uint64_t* words[Sets];                   // a tree's, of this lane's rows
+  u32x4 q[Sets][D / 32];
+  float c[Sets];
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    q[i] = u32x4{0, 0, 0, 0};
-    if (row < rows)
-      q[i] = *reinterpret_cast<const u32x4*>(a.q + qrow * a.ldq + (int64_t)head * D + F::q_at(i, g));
+  for (int x = 0; x < Sets; ++x) {
+    const int row = row0 + 16 * x + col, t = row / G;
+    const int64_t qrow = b * a.Lq + t;
+    const int head = hk * G + (row - t * G);
+    upto[x] = src.causal ? n - (nq - 1 - t) : n;
+    if constexpr (Source::kTree) words[x] = src.tree + b * src.stride + (int64_t)min(t, nq - 1) * src.words;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      q[x][i] = u32x4{0, 0, 0, 0};
+      if (row < rows)
+        q[x][i] = *reinterpret_cast<const u32x4*>(a.q + qrow * a.ldq + (int64_t)head * D + F::q_at(i, g));
+    }
+    c[x] = query_operand<kF16>(q[x], a.scale * kLog2e, src.k_scale(), [](float v) { return quad_max(v); });
   }
-  const float c = query_operand<kF16>(q, a.scale * kLog2e, src.k_scale(),
-                                      [](float v) { return quad_max(v); });
 
   char* const vlds = lds + wave * F::kLds;
-  f32x4 o[D / 16];
+  f32x4 o[Sets][D / 16];
+  float m[Sets], l[Sets];                        // m: largest product, before the scale
 #pragma unroll
-  for (int d = 0; d < D / 16; ++d) o[d] = f32x4{0, 0, 0, 0};
-  float m = -INFINITY, l = 0.0f;                 // m: largest product, before the scale
-
-  const uint64_t* words = nullptr;               // a tree's, of this lane's row
-  if constexpr (Source::kTree) words = src.tree + b * src.stride + (int64_t)min(t, nq - 1) * src.words;
+  for (int x = 0; x < Sets; ++x) {
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) o[x][d] = f32x4{0, 0, 0, 0};
+    m[x] = -INFINITY;
+    l[x] = 0.0f;
+  }
 
   typename F::Regs cur;
   typename Source::Look look = {};
@@ -316,16 +338,19 @@ attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gat
   }
   for (int ch = c0 + wave; ch < c1; ch += kFewWaves) {
     const int base = ch * kFewKeys;
-    f32x4 s[4];
+    f32x4 s[Sets][4];
 #pragma unroll
     for (int t4 = 0; t4 < 4; ++t4) {
       u32x4 k[D / 32];
       F::k_tile(cur, t4, k);
-      s[t4] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) s[t4] = mfma16<kF16>(k[i], q[i], s[t4]);
+      for (int x = 0; x < Sets; ++x) {
+        s[x][t4] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) s[x][t4] = mfma16<kF16>(k[i], q[x][i], s[x][t4]);
+      }
     }
-    F::stage_v(cur, vlds, lane);
+    F::template stage_v<Source::kTree>(cur, vlds, lane);
     const uint64_t seen = cur.seen;
     // the next step's loads, and what those of the one after need
     if (ch + kFewWaves < c1) {
@@ -334,40 +359,47 @@ attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gat
     }
     const bool whole = seen == ~0ull && base + kFewKeys <= all;
     if (!whole) {
-      uint64_t mine = seen;
-      if constexpr (Source::kTree) mine &= src.row_sees(words, base, all);
+#pragma unroll
+      for (int x = 0; x < Sets; ++x) {
+        uint64_t mine = seen;
+        if constexpr (Source::kTree) mine &= src.row_sees(words[x], base, all);
+#pragma unroll
+        for (int t4 = 0; t4 < 4; ++t4)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int key = 16 * t4 + 4 * g + r;
+            const bool on = ((mine >> key) & 1) && base + key < upto[x];
+            s[x][t4][r] = on ? s[x][t4][r] : -INFINITY;
+          }
+      }
+    }
+    float f[Sets];
+    u32x4 p[Sets][2];
+#pragma unroll
+    for (int x = 0; x < Sets; ++x) {
+      float top = m[x];
 #pragma unroll
       for (int t4 = 0; t4 < 4; ++t4)
+        top = max3(max3(top, s[x][t4][0], s[x][t4][1]), s[x][t4][2], s[x][t4][3]);
+      top = quad_max(top);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      f[x] = m[x] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m[x] - ref) * c[x]);
+      const float shift = kPBias<kF16> - ref * c[x];
+      m[x] = top;
+      l[x] *= f[x];
+#pragma unroll
+      for (int t4 = 0; t4 < 4; ++t4) {
+        float e[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int key = 16 * t4 + 4 * g + r;
-          const bool on = ((mine >> key) & 1) && base + key < upto;
-          s[t4][r] = on ? s[t4][r] : -INFINITY;
+          e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t4][r], c[x], shift));
         }
-    }
-    float top = m;
 #pragma unroll
-    for (int t4 = 0; t4 < 4; ++t4)
-      top = max3(max3(top, s[t4][0], s[t4][1]), s[t4][2], s[t4][3]);
-    top = quad_max(top);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - ref) * c);
-    const float shift = kPBias<kF16> - ref * c;
-    m = top;
-    l *= f;
-    u32x4 p[2];
-#pragma unroll
-    for (int t4 = 0; t4 < 4; ++t4) {
-      float e[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t4][r], c, shift));
-      }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t w = pack16<kF16>(e[2 * r], e[2 * r + 1]);
-        l = add_pair<kF16>(w, l);
-        p[t4 >> 1][2 * (t4 & 1) + r] = w;
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t w = pack16<kF16>(e[2 * r], e[2 * r + 1]);
+          l[x] = add_pair<kF16>(w, l[x]);
+          p[x][t4 >> 1][2 * (t4 & 1) + r] = w;
+        }
       }
     }
     wave_lds_order();
@@ -375,52 +407,62 @@ attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gat
     for (int d = 0; d < D / 16; ++d) {
       u32x4 v[2];
       F::v_tile(vlds, d, lane, v);
-      o[d] *= f;
-      o[d] = mfma16<kF16>(v[0], p[0], o[d]);
-      o[d] = mfma16<kF16>(v[1], p[1], o[d]);
+#pragma unroll
+      for (int x = 0; x < Sets; ++x) {
+        o[x][d] *= f[x];
+        o[x][d] = mfma16<kF16>(v[0], p[x][0], o[x][d]);
+        o[x][d] = mfma16<kF16>(v[1], p[x][1], o[x][d]);
+      }
     }
     wave_lds_order();
   }
-  l = quad_sum(l);
 
   // join the waves: every wave's sums to the common maximum
   __syncthreads();
-  if (g == 0) {
-    ml[0][wave][col] = m;
-    ml[1][wave][col] = l;
+#pragma unroll
+  for (int x = 0; x < Sets; ++x) {
+    l[x] = quad_sum(l[x]);
+    if (g == 0) {
+      ml[0][wave][16 * x + col] = m[x];
+      ml[1][wave][16 * x + col] = l[x];
+    }
   }
   __syncthreads();
-  float mt = ml[0][0][col];
-#pragma unroll
-  for (int w = 1; w < kFewWaves; ++w) mt = fmaxf(mt, ml[0][w][col]);
-  const float ref = mt == -INFINITY ? 0.0f : mt;
-  float lt = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kFewWaves; ++w) {
-    // (times zero, not left out: a sum that is NaN stays so)
-    const float mw = ml[0][w][col];
-    lt += ml[1][w][col] * (mw == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mw - ref) * c));
-  }
-  const float fw = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - ref) * c);
   float* const join = reinterpret_cast<float*>(lds);
 #pragma unroll
-  for (int d = 0; d < D / 16; ++d)
+  for (int x = 0; x < Sets; ++x) {
+    const int at = 16 * x + col;
+    float mt = ml[0][0][at];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      join[(wave * kFewRows + col) * (D + 4) + 16 * d + 4 * g + r] = o[d][r] * fw;
-  if (wave == 0 && g == 0) {
-    fin[0][col] = mt == -INFINITY ? mt : mt * c;
-    fin[1][col] = lt;
+    for (int w = 1; w < kFewWaves; ++w) mt = fmaxf(mt, ml[0][w][at]);
+    const float ref = mt == -INFINITY ? 0.0f : mt;
+    float lt = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) {
+      // (times zero, not left out: a sum that is NaN stays so)
+      const float mw = ml[0][w][at];
+      lt += ml[1][w][at] * (mw == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mw - ref) * c[x]));
+    }
+    const float fw = m[x] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m[x] - ref) * c[x]);
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        join[(wave * kRows + at) * (D + 4) + 16 * d + 4 * g + r] = o[x][d][r] * fw;
+    if (wave == 0 && g == 0) {
+      fin[0][at] = mt == -INFINITY ? mt : mt * c[x];
+      fin[1][at] = lt;
+    }
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < kFewRows * D / 2; x += 64 * kFewWaves) {
+  for (int x = threadIdx.x; x < kRows * D / 2; x += 64 * kFewWaves) {
     const int rr = x / (D / 2), d = 2 * (x - rr * (D / 2));
     if (row0 + rr >= rows) break;
     float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
     for (int w = 0; w < kFewWaves; ++w) {
-      v0 += join[(w * kFewRows + rr) * (D + 4) + d];
-      v1 += join[(w * kFewRows + rr) * (D + 4) + d + 1];
+      v0 += join[(w * kRows + rr) * (D + 4) + d];
+      v1 += join[(w * kRows + rr) * (D + 4) + d + 1];
     }
     const float mr = fin[0][rr], lr = fin[1][rr];
     const int tr = (row0 + rr) / G, hr = hk * G + (row0 + rr - tr * G);
@@ -500,18 +542,17 @@ attn_join_kernel(AttnArgs a, Source src, AttnSplit sp, int splits, Gate gate) {
 // MB at 4.7 TB/s).
 constexpr int64_t kFewBlocks = 1024, kFewBlocksWide = 256;
 
-int64_t tiles_of(int64_t B, int64_t Lq, int Hq, int Hkv) {
-  return B * Hkv * ((Lq * (Hq / Hkv) + kFewRows - 1) / kFewRows);
+int64_t tiles_of(int64_t Lq, int Hq, int Hkv, int sets) {
+  return (Lq * (Hq / Hkv) + sets * kFewRows - 1) / (sets * kFewRows);
 }
 
-// Splits wanted for keys up to L.  A step of a workgroup's waves takes about
+// Splits wanted of u tiles for keys up to L.  A step of a workgroup's waves takes about
 // 1.8 us of a nearly empty chip and the join 0.22 us a split, so of w steps
 // more than sqrt(8 w) splits cost more than they give (one stream of 32768: 32
 // splits 21 us, 64 25, 128 37).
-int64_t splits_of(int64_t B, int64_t Lq, int Hq, int Hkv, int64_t L, int64_t blocks) {
-  const int64_t tiles = tiles_of(B, Lq, Hq, Hkv);
+int64_t splits_of(int64_t u, int64_t L, int64_t blocks) {
   const int64_t w = (L + kFewKeys * kFewWaves - 1) / (kFewKeys * kFewWaves);
-  int64_t s = (blocks + tiles - 1) / tiles;
+  int64_t s = (blocks + u - 1) / u;
   s = s < w ? s : w;
   while (s > 1 && s * s > 8 * w) --s;
   if (s <= 1) return 1;
@@ -519,10 +560,22 @@ int64_t splits_of(int64_t B, int64_t Lq, int Hq, int Hkv, int64_t L, int64_t blo
   return (w + steps - 1) / steps;
 }
 
+// Sixteens of rows that a wave takes.  Two spare every second key's decoding, but
+// take twice the registers and make the steps longer: only where a SIMD has 20
+// steps of 64 keys of 128 elements, 40 of 64 (32 rows of a key head, 128 key heads of
+// 128, 16000 keys: 109 -> 87 us; 32 of them 39.1 and 39.7; 8 and 4000 keys 13.0 and
+// 16.3.  Heads of 64: 62 -> 57, 25.1 and 28.8, 11.6 and 13.2.  Four at a time, 64 rows:
+// 269 us where two take 212.)
+int sets_of(const AttnArgs& a, int64_t L) {
+  if (a.Lq * (a.Hq / a.Hkv) <= kFewRows) return 1;
+  const int64_t steps = a.B * a.Hkv * tiles_of(a.Lq, a.Hq, a.Hkv, 1) * ((L + kFewKeys - 1) / kFewKeys);
+  return steps * a.D >= (int64_t)1024 * 20 * 128 ? 2 : 1;
+}
+
 }  // namespace
 
 size_t attn_few_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
-  const int64_t s = splits_of(B, Lq, Hq, Hkv, L, kFewBlocks);    // (a source may take fewer)
+  const int64_t s = splits_of(B * Hkv * tiles_of(Lq, Hq, Hkv, 1), L, kFewBlocks);   // (a source may take fewer)
   return s > 1 ? s * AttnSplit::bytes(B * Lq * Hq, D) : 0;
 }
 
@@ -530,20 +583,27 @@ template <class Source>
 hipError_t launch_attn_few(const AttnArgs& a, const Source& src, int64_t L, void* ws,
                            size_t ws_bytes, hipStream_t stream) {
   const int64_t rows = a.B * a.Lq * a.Hq;
-  int64_t s = splits_of(a.B, a.Lq, a.Hq, a.Hkv, L, !Source::kF16 && a.D == 128 ? kFewBlocksWide : kFewBlocks);
+  const int sets = Source::kTree ? sets_of(a, L) : 1;
+  const int64_t tiles = tiles_of(a.Lq, a.Hq, a.Hkv, sets);
+  int64_t s = splits_of(a.B * a.Hkv * tiles, L, !Source::kF16 && a.D == 128 ? kFewBlocksWide : kFewBlocks);
   const int64_t fit = (int64_t)(ws_bytes / AttnSplit::bytes(rows, a.D));
   if (s > fit) s = fit > 1 ? fit : 1;
   const AttnSplit sp = AttnSplit::in(ws, s, rows, a.D);
-  const int64_t tiles = (a.Lq * (a.Hq / a.Hkv) + kFewRows - 1) / kFewRows;
   const dim3 grid((unsigned)(a.B * a.Hkv * tiles * s)), block(64 * kFewWaves);
   const Gate gt = current_gate();
   const auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, src, sp, (int)tiles, (int)s, gt);
   };
-  if (tiles == 1)
-    a.D == 64 ? go(attn_few_kernel<Source, 64, true>) : go(attn_few_kernel<Source, 128, true>);
-  else
-    a.D == 64 ? go(attn_few_kernel<Source, 64, false>) : go(attn_few_kernel<Source, 128, false>);
+  const auto of = [&](auto once) {
+    constexpr bool kOnce = decltype(once)::value;
+    if constexpr (Source::kTree)
+      if (sets > 1) {
+        a.D == 64 ? go(attn_few_kernel<Source, 64, kOnce, 2>) : go(attn_few_kernel<Source, 128, kOnce, 2>);
+        return;
+      }
+    a.D == 64 ? go(attn_few_kernel<Source, 64, kOnce, 1>) : go(attn_few_kernel<Source, 128, kOnce, 1>);
+  };
+  tiles == 1 ? of(std::true_type{}) : of(std::false_type{});
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || s == 1) return e;
   return launch_attn_join(a, src, sp, (int)s, stream);

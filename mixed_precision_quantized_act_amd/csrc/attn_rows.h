@@ -45,7 +45,7 @@ __device__ __forceinline__ int k_piece(int key, int c) {
 }
 template <int D>
 __device__ __forceinline__ int v_piece(int key, int c) {
-  return key * (D * 2) + 32 * ((c >> 1) ^ (D == 128 ? key & 7 : key & 3)) + 16 * (c & 1);
+  return key * (D * 2) + 32 * ((c >> 1) ^ (D == 128 ? 2 * (key & 3) + ((key >> 2) & 1) : key & 3)) + 16 * (c & 1);
 }
 
 // Before a row has seen a key: any logit plus this gives an infinite weight,

@@ -57,7 +57,7 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, Pieces pc, Gat
 
   // keys that every row of the wave sees, that any row of it and of the
   // workgroup sees
-  const int all = Source::kTree ? n - nq : src.causal ? n - (nq - 1 - row0 / G) : n;
+  const int all = src.causal ? n - (nq - 1 - row0 / G) : n;
   const int wend = wlast < row0 ? 0 : (src.causal ? n - (nq - 1 - wlast / G) : n);
   const int last = min(tile * (32 * W) + 32 * W, rows) - 1;
   const int end = src.causal ? n - (nq - 1 - last / G) : n;
@@ -97,8 +97,6 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, Pieces pc, Gat
   const int row = row0 + col, t = row / G;
   const int upto = src.causal ? n - (nq - 1 - t) : n;
   const int head = hk * G + row - t * G;
-  const uint64_t* words = nullptr;                 // a tree's, of this lane's row
-  if constexpr (Source::kTree) words = src.tree + b * src.stride + (int64_t)min(t, nq - 1) * src.words;
   Rows<kF16, D> r;
   {
     const uint16_t* p = a.q + (b * a.Lq + t) * a.ldq + (int64_t)head * D + 8 * h;
@@ -178,15 +176,13 @@ attn_tile_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, Pieces pc, Gat
   int i = 0;
   for (; i < mine; ++i) {
     const int base = base0 + i * kTileKeys;
-    uint64_t here = seen[0];
+    const uint64_t here = seen[0];
     const bool whole = here == ~0ull && base + kTileKeys <= all;
     // `va` is at the tile before (in the first there is none: zeros), `ka` at
     // this one; on to the next tile of K (after the last: logits that nobody
     // looks at) and to this one of V
     const int ks = slot == 2 ? -2 * kBytes : kBytes;
     const int vs = i == 0 ? -kZeros : slot == 0 ? -2 * kBytes : kBytes;
-    if constexpr (Source::kTree)
-      if (!whole) here &= src.row_sees(words, base, all);
     if (!whole) hide(s0, (uint32_t)here, upto - base, h);
     r.template step<kHalf, 0>(s0, p0, s1, p1, sum, ahead, kt, ka, vt, va, ks, vs,
                               [&](int turn) { store_turn(turn); });
@@ -263,8 +259,6 @@ hipError_t launch_attn_tile(const AttnArgs& a, const Source& src, int64_t L, voi
 }
 
 template hipError_t launch_attn_tile(const AttnArgs&, const Kv4Source&, int64_t, void*, size_t,
-                                     hipStream_t);
-template hipError_t launch_attn_tile(const AttnArgs&, const Kv4TreeSource&, int64_t, void*, size_t,
                                      hipStream_t);
 template hipError_t launch_attn_tile(const AttnArgs&, const CrossSource&, int64_t, void*, size_t,
                                      hipStream_t);
