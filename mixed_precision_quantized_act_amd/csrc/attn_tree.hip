@@ -26,9 +26,10 @@ constexpr int tree_rows(int parts) { return 32 * kTreeWaves / parts; }
 // rows do not see, whose weight of zero needs a number (no scale is negative).
 constexpr uint32_t kMostScale = 0x7E;
 
-// Sums of a part of the keys.  Shares of the list: share w has at most two, 2 w, of a unit
-// that began in an earlier one, and 2 w + 1, of one that goes on in the next.  Equal
-// pieces: one each, unit u's are u pieces ..
+// Sums of a part of the keys.  Shares of the list: share w's own are of a unit that began
+// in an earlier one; behind all shares' stand those of a unit that goes on in the next
+// (of unit u at u, or with more units than shares at w).  Equal pieces: one each, unit
+// u's are u pieces ..
 struct TreeSums {
   float* o;       // [sums][rows of a tile][D]
   float* m;       // [sums][rows] largest logit (log2 units), -inf: nothing seen
@@ -36,6 +37,7 @@ struct TreeSums {
   i32x2* cut;     // [units] the share in which a unit begins, and ends (the same: nothing to join)
   int shares;     // of the list; 0: equal pieces
   int pieces;
+  int by_unit;    // units <= shares
 
   static size_t bytes(int64_t sums, int64_t cuts, int rows, int D) {
     return (size_t)(sums * rows * (D + 2) * 4 + cuts * 8);
@@ -171,9 +173,9 @@ attn_tree_kernel(AttnArgs a, Kv4TreeSource src, TreeSums sp, int tiles, Gate gat
   asm volatile("" : "+v"(lane));
   const int col = lane & 31, h = lane >> 5;
   const int len = tree_len(n), c1 = min(len, c0 + stop - at);
+  const int unit = ((int)b * a.Hkv + hk) * tiles + tile;
   if (sp.shares && c0 == 0 && tid == 0)
-    sp.cut[(b * a.Hkv + hk) * tiles + tile] =
-        i32x2{(int)blockIdx.x, c1 == len ? (int)blockIdx.x : list.last(at, len)};
+    sp.cut[unit] = i32x2{(int)blockIdx.x, c1 == len ? (int)blockIdx.x : list.last(at, len)};
   const int rows = nq * G;
   const int row0 = tile * kRows + group * 32;
   const bool mine = row0 < rows;                           // this wave has rows
@@ -448,7 +450,7 @@ attn_tree_kernel(AttnArgs a, Kv4TreeSource src, TreeSums sp, int tiles, Gate gat
     if (sp.shares ? c1 - c0 == len : sp.pieces == 1) {
       store_rows(r, src.v_scale(), a.o + (b * a.Lq + t) * a.ldo + (int64_t)head * D, h, row < rows);
     } else if (row < rows) {
-      const int64_t to = (int64_t)(sp.shares ? 2 * blockIdx.x + (c0 == 0 ? 1 : 0) : blockIdx.x) * kRows + group * 32 + col;
+      const int64_t to = (int64_t)((int)blockIdx.x + (sp.shares && c0 == 0 ? sp.shares + (sp.by_unit ? unit - (int)blockIdx.x : 0) : 0)) * kRows + group * 32 + col;
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
 #pragma unroll
@@ -491,16 +493,17 @@ join_tree_kernel(AttnArgs a, Kv4TreeSource src, TreeSums sp, int tiles, Gate gat
   const int head = (int)((uint32_t)at - qrow * a.Hq), t = (int)(qrow - b * (uint32_t)a.Lq), G = a.Hq / a.Hkv;
   const int hk = head / G, row = t * G + head - hk * G;
   const int unit = (b * a.Hkv + hk) * tiles + row / kRows;
-  int w0 = 2 * unit * sp.pieces, w1 = w0 + 2 * sp.pieces - 2;
+  int w0 = unit * sp.pieces, w1 = w0 + sp.pieces - 1, from = w0;
   if (sp.shares) {
     const i32x2 cut = sp.cut[unit];                        // (of a row that is there)
-    w0 = 2 * cut[0] + 1;
-    w1 = 2 * cut[1];
+    w0 = cut[0];
+    w1 = cut[1];
+    from = sp.shares + (sp.by_unit ? unit : w0);
   }
-  if (t >= src.queries(b, a.Lq) || w1 < w0) return;
+  if (t >= src.queries(b, a.Lq) || w0 == w1) return;
   float mt = -INFINITY, l = 0.0f;
   f32x4 o = {0, 0, 0, 0};
-  for (int s0 = w0 / 2; s0 <= w1 / 2; s0 += kTurn) {
+  for (int s0 = w0; s0 <= w1; s0 += kTurn) {
     float ms[kTurn], ls[kTurn];
     f32x4 os[kTurn];
     float top = mt;
@@ -509,8 +512,8 @@ join_tree_kernel(AttnArgs a, Kv4TreeSource src, TreeSums sp, int tiles, Gate gat
       ms[j] = -INFINITY;
       ls[j] = 0.0f;
       os[j] = f32x4{0, 0, 0, 0};
-      if (s0 + j <= w1 / 2) {
-        const int64_t i = (int64_t)(sp.shares ? max(2 * (s0 + j), w0) : s0 + j) * kRows + row % kRows;
+      if (s0 + j <= w1) {
+        const int64_t i = (int64_t)(s0 + j == w0 ? from : s0 + j) * kRows + row % kRows;
         ms[j] = sp.m[i];
         ls[j] = sp.l[i];
         os[j] = *reinterpret_cast<const f32x4*>(sp.o + i * D + d);
@@ -537,8 +540,8 @@ join_tree_kernel(AttnArgs a, Kv4TreeSource src, TreeSums sp, int tiles, Gate gat
       u32x2{bf16_pack(o[0] * f, o[1] * f), bf16_pack(o[2] * f, o[3] * f)};
 }
 
-// One workgroup fits a compute unit: this many shares.
-constexpr int64_t kShares = 256;
+// One workgroup fits a compute unit: this many run at once.
+constexpr int kPlaces = 256;
 constexpr int kPieces = 16;
 
 // Rows up to which a tile is of two parts.
@@ -562,37 +565,44 @@ double tree_join_time(int64_t sums, int rows, int D) { return 4.0 + (double)sums
 // and 180; of 8000: 56 and 59; of 4000: 37 and 40).
 struct TreeCut {
   int shares, pieces;
+  int64_t sums;
   size_t bytes;
 };
 TreeCut tree_cut(int64_t units, int rows, int D, int parts, int64_t len, size_t ws_bytes) {
-  TreeCut best = {0, 1, 0};
+  TreeCut best = {0, 1, 0, 0};
   const double each = tree_tile_time(D, parts);
-  double least = (double)((units + kShares - 1) / kShares) * ((double)len * each + kUnitStart);
-  for (int n = 2; n <= kPieces && n <= len; ++n) {
-    const size_t bytes = TreeSums::bytes(units * n, 0, rows, D);
-    if (bytes > ws_bytes || units * n > 8 * kShares) break;
-    const double t = (double)((units * n + kShares - 1) / kShares) * ((double)((len + n - 1) / n) * each + kUnitStart) +
+  double least = (double)((units + kPlaces - 1) / kPlaces) * ((double)len * each + kUnitStart);
+  const auto take = [&](int shares, int pieces, int64_t sums) {
+    best = {shares, pieces, sums, TreeSums::bytes(sums, shares ? units : 0, rows, D)};
+  };
+  for (int n = 2; n <= kPieces && n <= len && units * n <= 8 * kPlaces; ++n) {
+    if (TreeSums::bytes(units * n, 0, rows, D) > ws_bytes) break;
+    const double t = (double)((units * n + kPlaces - 1) / kPlaces) * ((double)((len + n - 1) / n) * each + kUnitStart) +
                      tree_join_time(units * n, rows, D);
     if (t < least) {
       least = t;
-      best = {0, n, bytes};
+      take(0, n, units * n);
     }
   }
-  const size_t bytes = TreeSums::bytes(2 * kShares, units, rows, D);
-  if (units < 8 * kShares && units * len * kShares < (int64_t)1 << 31 && bytes <= ws_bytes) {
-    const double per = (double)units / kShares;
-    const double t = kListTime + per * (double)len * each + (1.0 + per) * kUnitStart +
-                     tree_join_time(units + kShares, rows, D);
-    if (t < 1.1 * least) best = {(int)kShares, 0, bytes};
+  if (units >= 8 * kPlaces || units * len * kPlaces >= (int64_t)1 << 31) return best;
+  for (int shares = kPlaces; shares >= kPlaces / 2; shares -= 16) {
+    const int64_t sums = shares + (units < shares ? units : shares);
+    if (TreeSums::bytes(sums, units, rows, D) > ws_bytes) continue;
+    const double per = (double)units / shares;
+    const double t = kListTime + per * (double)len * each + (1.0 + per) * kUnitStart + tree_join_time(sums, rows, D);
+    if (t < 1.1 * least) take(shares, 0, sums);
+    break;
   }
   return best;
 }
 
 }  // namespace
 
+// (asked for: at most 32 MiB, whatever more would give)
 size_t attn_tree_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
   const int parts = parts_of(Lq, Hq, Hkv);
-  return tree_cut(units_of(B, Lq, Hq, Hkv), tree_rows(parts), D, parts, (L + kTileKeys - 1) / kTileKeys, SIZE_MAX).bytes;
+  return tree_cut(units_of(B, Lq, Hq, Hkv), tree_rows(parts), D, parts, (L + kTileKeys - 1) / kTileKeys,
+                  (size_t)32 << 20).bytes;
 }
 
 hipError_t launch_attn_tree(const AttnArgs& a, const Kv4TreeSource& src, int64_t L, void* ws, size_t ws_bytes,
@@ -601,15 +611,15 @@ hipError_t launch_attn_tree(const AttnArgs& a, const Kv4TreeSource& src, int64_t
   const int parts = parts_of(a.Lq, a.Hq, a.Hkv), rows = tree_rows(parts);
   const int64_t units = units_of(a.B, a.Lq, a.Hq, a.Hkv);
   const TreeCut c = tree_cut(units, rows, a.D, parts, (L + kTileKeys - 1) / kTileKeys, ws_bytes);
-  const int64_t sums = c.shares ? 2 * c.shares : units * c.pieces;
   TreeSums sp = {};
   sp.shares = c.shares;
   sp.pieces = c.pieces;
+  sp.by_unit = units <= c.shares;
   if (c.bytes) {
     sp.o = static_cast<float*>(ws);
-    sp.m = sp.o + sums * rows * a.D;
-    sp.l = sp.m + sums * rows;
-    sp.cut = reinterpret_cast<i32x2*>(sp.l + sums * rows);
+    sp.m = sp.o + c.sums * rows * a.D;
+    sp.l = sp.m + c.sums * rows;
+    sp.cut = reinterpret_cast<i32x2*>(sp.l + c.sums * rows);
   }
   const dim3 grid((unsigned)(c.shares ? c.shares : units * c.pieces)), block(kTreeThreads);
   const int tiles = (int)(units / (a.B * a.Hkv));

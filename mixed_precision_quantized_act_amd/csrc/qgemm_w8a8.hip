@@ -488,16 +488,6 @@ hipError_t launch_w8a8(const int8_t* a_q, const float* a_s, const int8_t* w_q, c
   g.part = static_cast<int32_t*>(ws);
   g.gate = current_gate();
   const W8Plan p = w8_plan(M, N, K, ws_bytes);
-#ifdef FORCE
-  const W8Plan q = FORCE; 
-  if (q.split) return launch_w8a8_split(q.shape, q.cuts, g, e, st);
-  switch (q.shape) {
-    case kTile128: return launch<Shape<1, 4, 4>>(g, q.streamed, e, st);
-    case kTile256x128: return launch<Shape<2, 4, 4>>(g, q.streamed, e, st);
-    case kTile192x256: return launch<Shape<3, 2, 4>>(g, q.streamed, e, st);
-    default: return launch<Large>(g, q.streamed, e, st);
-  }
-#endif
   if (p.split) return launch_w8a8_split(p.shape, p.cuts, g, e, st);
   switch (p.shape) {
     case kTile128: return launch<Shape<1, 4, 4>>(g, p.streamed, e, st);

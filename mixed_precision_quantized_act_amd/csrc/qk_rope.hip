@@ -12,7 +12,12 @@
 //
 // The bound is the memory rate, 4 bytes per element.  A workgroup takes whole
 // tokens, forms each token's R/2 sines and cosines once, in shared memory, for
-// all its heads, and has the heads' elements on their way meanwhile.
+// all its heads, and has the heads' elements on their way meanwhile: one thread two
+// vectors, so that many small workgroups hide each other's waits.  17776 tokens of 30 +
+// 30 heads of 64 (273 MB): 50 us, 5.4 TB/s, where a large copy reaches 5.1; workgroups of 64,
+// 256 and 512 threads 54, 52 and 52; four times the vectors a thread 57; stores past the
+// caches 73 (half the head turned) and 54 (all of it).  63 tokens of 32 + 8 heads of 128: 5 us,
+// a launch.
 #include "qact_device.h"
 #include "qact_internal.h"
 
@@ -20,109 +25,89 @@ namespace qact {
 
 namespace {
 
-constexpr int kRopeMost = 2048;        // sines and cosines of a workgroup's tokens
+constexpr int kRopeThreads = 128;
+constexpr int kRopeMost = 8 * kRopeThreads;        // sines and cosines of a workgroup's tokens
 
 // A thread's work: 16 elements of a head, two vectors of 8: j < R / 16 the
 // vectors j and j + R / 16 of the turned part (the two halves' partners, or 8
 // pairs), above them two neighbouring vectors that are passed on.
-template <int U>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kRopeThreads)
 qk_rope_kernel(RopeArgs a, int per, int tokens, Gate gate) {
   if (gated_off(gate)) return;
   __shared__ float2 table[kRopeMost];
-  __shared__ int turned[64];
+  __shared__ int turned[kRopeThreads];
   const int tid = threadIdx.x, half = a.R / 2;
   const int64_t m0 = (int64_t)blockIdx.x * tokens;
   const int here = (int)min<int64_t>(tokens, a.M - m0);
-  const int units = a.D / 16, rot = a.R / 16, total = here * per;
-  const int begin = blockIdx.y * (256 * U);
+  const int units = a.D / 16, rot = a.R / 16;
 
-  u32x4 w0[U], w1[U];
-  uint16_t* dst[U];
-  int place[U];                        // table entry of the first pair; -1: passed on, -2: nothing
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int i = begin + u * 256 + tid;
-    place[u] = -2;
-    if (i >= total) continue;
-    const int t = i / per, x = i - t * per, h = x / units, j = x - h * units;
-    const bool key = h >= a.Hq;
-    const int64_t m = m0 + t;
-    const int first = j < rot ? j : 2 * rot + 2 * (j - rot), second = j < rot ? j + rot : first + 1;
-    const int64_t at = (int64_t)(key ? h - a.Hq : h) * a.D + 8 * first;
+  const int i = blockIdx.y * kRopeThreads + tid, t = i / per, x = i - t * per, h = x / units, j = x - h * units;
+  const bool on = t < here, key = h >= a.Hq;
+  const int first = j < rot ? j : 2 * rot + 2 * (j - rot), apart = j < rot ? 8 * rot : 8;
+  const int64_t m = m0 + t, at = (int64_t)(key ? h - a.Hq : h) * a.D + 8 * first;
+  u32x4 w0 = {0, 0, 0, 0}, w1 = w0;
+  if (on) {
     const uint16_t* src = (key ? a.k + m * a.ldk : a.q + m * a.ldq) + at;
-    dst[u] = (key ? a.k_out + m * a.ldko : a.q_out + m * a.ldqo) + at;
-    w0[u] = *reinterpret_cast<const u32x4*>(src);
-    w1[u] = *reinterpret_cast<const u32x4*>(src + 8 * (second - first));
-    place[u] = j < rot ? t * half + (a.rope == QA_ROPE_PAIRS ? 4 * j : 8 * j) : -1;
+    w0 = *reinterpret_cast<const u32x4*>(src);
+    w1 = *reinterpret_cast<const u32x4*>(src + apart);
   }
 
-  for (int x = tid; x < here * half; x += 256) {
-    const int t = x / half, i = x - t * half;
-    const int pos = a.pos ? a.pos[m0 + t] : (int)(m0 + t);
-    const double turns = (double)pos * a.freq[i] * 0.15915494309189535;      // 1 / (2 pi)
-    const float f = (float)(2.0 * (turns - rint(turns)));
+  for (int y = tid; y < here * half; y += kRopeThreads) {
+    const int n = y / half, f = y - n * half;
+    const int pos = a.pos ? a.pos[m0 + n] : (int)(m0 + n);
+    const double turns = (double)pos * a.freq[f] * 0.15915494309189535;      // 1 / (2 pi)
     float s, c;
-    sincospif(f, &s, &c);
-    table[x] = float2{c * a.scale, s * a.scale};
-    if (i == 0) turned[t] = pos >= 0;
+    sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+    table[y] = float2{c * a.scale, s * a.scale};
+    if (f == 0) turned[n] = pos >= 0;
   }
   __syncthreads();
+  if (!on) return;
 
+  if (j < rot && turned[t]) {
+    float u[8], v[8];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (place[u] == -2) continue;
-    const int second = place[u] >= 0 ? a.R / 2 : 8;
-    if (place[u] >= 0 && turned[place[u] / half]) {
-      float x[8], y[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(w0[u][i]);
-        x[2 * i + 1] = bf16_hi(w0[u][i]);
-        y[2 * i] = bf16_lo(w1[u][i]);
-        y[2 * i + 1] = bf16_hi(w1[u][i]);
-      }
-      const float2* cs = table + place[u];
-      if (a.rope == QA_ROPE_PAIRS) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 p = cs[i], q = cs[half / 2 + i];
-          const float u0 = x[2 * i], v0 = x[2 * i + 1], u1 = y[2 * i], v1 = y[2 * i + 1];
-          x[2 * i] = __builtin_fmaf(u0, p.x, -(v0 * p.y));
-          x[2 * i + 1] = __builtin_fmaf(v0, p.x, u0 * p.y);
-          y[2 * i] = __builtin_fmaf(u1, q.x, -(v1 * q.y));
-          y[2 * i + 1] = __builtin_fmaf(v1, q.x, u1 * q.y);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 p = cs[i];
-          const float u0 = x[i], v0 = y[i];
-          x[i] = __builtin_fmaf(u0, p.x, -(v0 * p.y));
-          y[i] = __builtin_fmaf(v0, p.x, u0 * p.y);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w0[u][i] = bf16_pack(x[2 * i], x[2 * i + 1]);
-        w1[u][i] = bf16_pack(y[2 * i], y[2 * i + 1]);
-      }
+    for (int k = 0; k < 4; ++k) {
+      u[2 * k] = bf16_lo(w0[k]);
+      u[2 * k + 1] = bf16_hi(w0[k]);
+      v[2 * k] = bf16_lo(w1[k]);
+      v[2 * k + 1] = bf16_hi(w1[k]);
     }
-    *reinterpret_cast<u32x4*>(dst[u]) = w0[u];
-    *reinterpret_cast<u32x4*>(dst[u] + second) = w1[u];
+    const float2* cs = table + t * half;
+    const auto turn = [](float& a, float& b, float2 p) {
+      const float a0 = a, b0 = b;
+      a = __builtin_fmaf(a0, p.x, -(b0 * p.y));
+      b = __builtin_fmaf(b0, p.x, a0 * p.y);
+    };
+    if (a.rope == QA_ROPE_PAIRS) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        turn(u[2 * k], u[2 * k + 1], cs[4 * j + k]);
+        turn(v[2 * k], v[2 * k + 1], cs[4 * j + half / 2 + k]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) turn(u[k], v[k], cs[8 * j + k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      w0[k] = bf16_pack(u[2 * k], u[2 * k + 1]);
+      w1[k] = bf16_pack(v[2 * k], v[2 * k + 1]);
+    }
   }
+  uint16_t* dst = (key ? a.k_out + m * a.ldko : a.q_out + m * a.ldqo) + at;
+  *reinterpret_cast<u32x4*>(dst) = w0;
+  *reinterpret_cast<u32x4*>(dst + apart) = w1;
 }
 
 }  // namespace
 
 hipError_t launch_qk_rope(const RopeArgs& a, hipStream_t stream) {
   const int per = (a.Hq + a.Hk) * (a.D / 16);              // of a token
-  int tokens = 1024 / per;
-  if (tokens > kRopeMost / (a.R / 2)) tokens = kRopeMost / (a.R / 2);
-  if (tokens > 64) tokens = 64;
-  if (tokens < 1) tokens = 1;
-  const dim3 grid((unsigned)((a.M + tokens - 1) / tokens), (unsigned)((tokens * per + 1023) / 1024));
-  hipLaunchKernelGGL(qk_rope_kernel<4>, grid, dim3(256), 0, stream, a, per, tokens, current_gate());
+  const int most = kRopeMost / (a.R / 2), fit = kRopeThreads / per;
+  const int tokens = fit < 1 ? 1 : fit < most ? fit : most;
+  const dim3 grid((unsigned)((a.M + tokens - 1) / tokens), (unsigned)((tokens * per + kRopeThreads - 1) / kRopeThreads));
+  hipLaunchKernelGGL(qk_rope_kernel, grid, dim3(kRopeThreads), 0, stream, a, per, tokens, current_gate());
   return hipGetLastError();
 }
 

@@ -116,7 +116,7 @@ def test_rope_freqs_refusals():
 
 def test_workspace_sizes():
     for B, Lq, Hq, H, L in ((1, 1, 30, 30, 12376), (16, 32, 32, 8, 32768), (3, 250, 30, 30, 8191)):
-        assert 0 <= qa.attn_kv4_tree_workspace(B, Lq, Hq, H, 64, L) <= 80 << 20
+        assert 0 <= qa.attn_kv4_tree_workspace(B, Lq, Hq, H, 64, L) <= 32 << 20
     for bad in ((1, 1025, 4, 2, 64, 10), (-1, 1, 4, 2, 64, 10), (1, 1, 3, 2, 64, 10), (1, 1, 4, 2, 80, 10)):
         assert qa.attn_kv4_tree_workspace(*bad) == 0
     for M, N, K in ((1, 16384, 8192), (64, 7680, 1920), (17776, 5760, 1920), (300, 257, 131056), (1, 1, 16)):

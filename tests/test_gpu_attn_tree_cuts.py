@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 
 def _kind(B, T, Hq, H, D, cols):
-    """Which cut the workspace's size tells of (256 shares of two sums; n pieces of a unit, one each)."""
+    """Which cut the workspace's size tells of (shares' sums and units'; n pieces of a unit, one each)."""
     rows = T * (Hq // H)
     assert rows > 48 and B * H * -(-rows // 16) * -(-cols // 64) > 6 * 1024
     assert rows > 64 or B * H * -(-rows // 16) * -(-cols // 64) < 64 * 1024
@@ -20,10 +20,11 @@ def _kind(B, T, Hq, H, D, cols):
     units, n = B * H * -(-rows // tile), _qa().attn_kv4_tree_workspace(B, T, Hq, H, D, cols)
     if n == 0:
         return "whole"
-    if n == 512 * tile * (D + 2) * 4 + units * 8:
-        return "shares"
-    assert n % (units * tile * (D + 2) * 4) == 0
-    return "pieces"
+    if n % (units * tile * (D + 2) * 4) == 0:
+        return "pieces"
+    shares = (n - units * 8) // (tile * (D + 2) * 4) - units
+    assert 128 <= shares <= 256 and (n - units * 8) % (tile * (D + 2) * 4) == 0
+    return "shares"
 
 
 def _cols(lens, extra, page):
