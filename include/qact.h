@@ -573,7 +573,8 @@ int attn_kv4(const uint16_t* q, int64_t ldq, int64_t B, int64_t Lq, int Hq, int 
  * tree[b tree_stride + t W + j / 64] is set, W = ceil(Lq / 64) (u64, 8-byte
  * aligned; tree_stride in words, at least Lq W, or 0: one tree for all streams).
  * Bits of tokens from q_lens[b] on are ignored; a row that sees nothing gives
- * zeros.  Lq <= 1024.  Everything else, the workspace too, as for attn_kv4.
+ * zeros; what a token holds that a row does not see changes nothing of that row
+ * (NaN's scales included).  Lq <= 1024.  Everything else, the workspace too, as for attn_kv4.
  *
  * kv4_keep: the tokens of a checked tree that are kept move to the front of the
  * drafted positions: the codes and scales of position start[b] + path[b T + i]

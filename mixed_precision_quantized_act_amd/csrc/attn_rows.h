@@ -38,7 +38,9 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // Position of 16-byte piece c of key `key` in a staged tile (bytes).  K is
 // read as 16-byte pieces of 32 keys, V as 32-byte pieces of 8 keys; the
-// exchange among a key's pieces spreads either over all banks.
+// exchange among a key's pieces spreads either over all banks.  (V of 128: two
+// pieces of four keys are read at once, so keys 4 k .. 4 k + 3 differ in the exchange's
+// upper bits; by key % 8 they would meet, 291 against 283 us for 128 rows of a tree.)
 template <int D>
 __device__ __forceinline__ int k_piece(int key, int c) {
   return key * (D * 2) + 16 * (c ^ (D == 128 ? key & 15 : (key >> 1) & 7));

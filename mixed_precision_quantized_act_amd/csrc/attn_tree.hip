@@ -558,7 +558,7 @@ int64_t units_of(int64_t B, int64_t Lq, int Hq, int Hkv) {
   return B * Hkv * ((Lq * (Hq / Hkv) + rows - 1) / rows);
 }
 
-// us: a unit's start and end; a tile of keys; the list; what sums cost, written and
+// us: a unit's start and end; a tile of keys; 64 streams of the list; what sums cost, written and
 // read again at 4 TB/s, and the launch that joins them.
 constexpr double kUnitStart = 10.0, kListTime = 5.0;
 double tree_tile_time(int D, int parts) { return D == 64 ? (parts == 2 ? 0.8 : 1.1) : (parts == 2 ? 1.25 : 1.9); }
@@ -575,7 +575,7 @@ struct TreeCut {
   int64_t sums;
   size_t bytes;
 };
-TreeCut tree_cut(int64_t units, int rows, int D, int parts, int64_t len, size_t ws_bytes) {
+TreeCut tree_cut(int64_t B, int64_t units, int rows, int D, int parts, int64_t len, size_t ws_bytes) {
   TreeCut best = {0, 1, 0, 0};
   const double each = tree_tile_time(D, parts);
   double least = (double)((units + kPlaces - 1) / kPlaces) * ((double)len * each + kUnitStart);
@@ -596,7 +596,7 @@ TreeCut tree_cut(int64_t units, int rows, int D, int parts, int64_t len, size_t 
     const int64_t sums = shares + (units < shares ? units : shares);
     if (TreeSums::bytes(sums, units, rows, D) > ws_bytes) continue;
     const double per = (double)units / shares;
-    const double t = kListTime + per * (double)len * each + (1.0 + per) * kUnitStart + tree_join_time(sums, rows, D);
+    const double t = kListTime * (double)((B + 63) / 64) + per * (double)len * each + (1.0 + per) * kUnitStart + tree_join_time(sums, rows, D);
     if (t < 1.1 * least) take(shares, 0, sums);
     break;
   }
@@ -608,7 +608,7 @@ TreeCut tree_cut(int64_t units, int rows, int D, int parts, int64_t len, size_t 
 // (asked for: at most 32 MiB, whatever more would give)
 size_t attn_tree_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
   const int parts = parts_of(Lq, Hq, Hkv);
-  return tree_cut(units_of(B, Lq, Hq, Hkv), tree_rows(parts), D, parts, (L + kTileKeys - 1) / kTileKeys,
+  return tree_cut(B, units_of(B, Lq, Hq, Hkv), tree_rows(parts), D, parts, (L + kTileKeys - 1) / kTileKeys,
                   (size_t)32 << 20).bytes;
 }
 
@@ -617,7 +617,7 @@ hipError_t launch_attn_tree(const AttnArgs& a, const Kv4TreeSource& src, int64_t
   const Gate gt = current_gate();
   const int parts = parts_of(a.Lq, a.Hq, a.Hkv), rows = tree_rows(parts);
   const int64_t units = units_of(a.B, a.Lq, a.Hq, a.Hkv);
-  const TreeCut c = tree_cut(units, rows, a.D, parts, (L + kTileKeys - 1) / kTileKeys, ws_bytes);
+  const TreeCut c = tree_cut(a.B, units, rows, a.D, parts, (L + kTileKeys - 1) / kTileKeys, ws_bytes);
   TreeSums sp = {};
   sp.shares = c.shares;
   sp.pieces = c.pieces;

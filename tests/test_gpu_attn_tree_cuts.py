@@ -165,6 +165,66 @@ def test_captured_and_replayed_beside_another(D, T):
         assert t.equal(o, want[i]) and t.equal(p, want[j])
 
 
+@pytest.mark.parametrize("D,T", [(64, 60), (128, 100), (64, 200), (128, 150)])
+def test_queries_that_are_not_finite_stay_with_their_row(D, T):
+    """A token's NaN or infinity reaches its own row only, where waves' and shares' sums are joined, too."""
+    qa, t = _qa(), torch()
+    case = CacheCase(34, 1, 1, D, 64, [3000], extra_pages=2000)
+    parts, lens = case.device(dev), dev(np.array([3000], np.int32))
+    q = t.randn((T, 2 * D), device="cuda", generator=t.Generator(device="cuda").manual_seed(7)).bfloat16()
+    word = dev(O.words(O.ancestors([-1] * T)))
+    n = qa.attn_kv4_tree_workspace(1, T, 2, 1, D, case.cache.table.shape[1] * 64)
+    out = []
+    for bad in (None, float("nan"), float("inf")):
+        x, o = q.clone(), t.empty_like(q)
+        if bad is not None:
+            x[1, D + 7] = bad
+        qa.attn_kv4_tree(x, *parts, lens, word, o, 1, T, 2, ws=_ws(n))
+        out.append(o)
+    mask = t.ones_like(q, dtype=t.bool)
+    mask[1, D:] = False
+    for o in out[1:]:
+        assert not bool(o[1, D:].isfinite().any()) and bool(o[mask].isfinite().all())
+        # (the other rows' references may move with their tile: within their roundings)
+        assert float((o[mask].float() - out[0][mask].float()).abs().max()) <= 2.0 ** -6 * float(out[0].abs().max())
+
+
+_Short = CacheCase
+
+
+class _Long(_Short):
+    """A table of `to` entries a stream, those behind the cache's pages of no page."""
+    to = 1 << 14
+
+    def __init__(self, *a, **kw):
+        super().__init__(*a, **kw)
+        at = self.cache.table
+        self.cache.table = np.pad(at, ((0, 0), (0, self.to - at.shape[1])), constant_values=-1)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,Hq,H", [(17, 1, 1), (8, 4, 1), (31, 2, 2), (12, 4, 1), (16, 4, 1), (63, 1, 1)])
+def test_two_sixteens_of_rows_a_wave(monkeypatch, D, T, Hq, H):
+    """Few rows of a key head over very long tables (the lengths are short, so most splits are empty)."""
+    import tests.test_gpu_attn_tree as m
+    monkeypatch.setattr(m, "CacheCase", _Long)
+    rows, lens = T * (Hq // H), [3000, T, T + 70]
+    assert 3 * H * -(-rows // 16) * (_Long.to * 64 // 64) * D >= 1024 * 20 * 128 and rows > 16
+    assert rows <= 48 or 3 * H * -(-rows // 16) * _Long.to >= 64 * 1024
+    _tree(35, 3, T, Hq, H, D, 64, lens)
+    _tree(35, 3, T, Hq, H, D, 64, lens, q_lens=[T, 0, 1], kind="bits", ws=0)
+    _tree(36, 3, T, Hq, H, D, 64, [T + 500, 3, 0], kind="bits", ws=1_000_000)
+
+
+def test_two_sixteens_hide_any_bytes_and_other_rows(monkeypatch):
+    import tests.test_gpu_attn_tree as m
+    for cls in (m, __import__(__name__, fromlist=["x"])):
+        monkeypatch.setattr(cls, "CacheCase", _Long)
+    for D in (64, 128):
+        test_a_token_that_a_row_does_not_see_may_hold_any_bytes(D, 20, 1)
+    m.test_queries_that_are_not_finite_stay_with_their_row(20)
+
+
 def test_gate():
     qa, t = _qa(), torch()
     for T, H in ((60, 1), (100, 8), (65, 32)):
