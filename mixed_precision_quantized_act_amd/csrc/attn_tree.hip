@@ -177,315 +177,319 @@ attn_tree_kernel(AttnArgs a, Kv4TreeSource src, TreeSums sp, int tiles, Gate gat
     stop = (int)((int64_t)len * (piece + 1) / sp.pieces);
   }
   for (;;) {
-  // (a new value each time: the places that follow from it would be kept in registers
-  // beside a unit's, and those of 128 spill)
-  int lane = tid & 63;
-  asm volatile("" : "+v"(lane));
-  const int col = lane & 31, h = lane >> 5;
-  const int len = tree_len(n), c1 = min(len, c0 + stop - at);
-  const int unit = ((int)b * a.Hkv + hk) * tiles + tile;
-  if (sp.shares && c0 == 0 && tid == 0)
-    sp.cut[unit] = i32x2{(int)blockIdx.x, c1 == len ? (int)blockIdx.x : list.last(at, len)};
-  const int rows = nq * G;
-  const int row0 = tile * kRows + group * 32;
-  const bool mine = row0 < rows;                           // this wave has rows
-  const int all = n - nq;                                  // keys that every row sees
-  const int base0 = c0 * kTileKeys, nt = n > 0 ? c1 - c0 : 0;
+    // (a new value each time: the places that follow from it would be kept in registers
+    // beside a unit's, and those of 128 spill)
+    int lane = tid & 63;
+    asm volatile("" : "+v"(lane));
+    const int col = lane & 31, h = lane >> 5;
+    const int len = tree_len(n), c1 = min(len, c0 + stop - at);
+    const int unit = ((int)b * a.Hkv + hk) * tiles + tile;
+    if (sp.shares && c0 == 0 && tid == 0)
+      sp.cut[unit] = i32x2{(int)blockIdx.x, c1 == len ? (int)blockIdx.x : list.last(at, len)};
+    const int rows = nq * G;
+    const int row0 = tile * kRows + group * 32;
+    const bool mine = row0 < rows;                           // this wave has rows
+    const int all = n - nq;                                  // keys that every row sees
+    const int base0 = c0 * kTileKeys, nt = n > 0 ? c1 - c0 : 0;
 
-  const int row = row0 + col, t = row / G;
-  const int head = hk * G + row - t * G;
-  const uint64_t* const words = src.tree + b * src.stride + (int64_t)min(t, nq - 1) * src.words;
-  R r;
-  {
-    const uint16_t* p = a.q + (b * a.Lq + t) * a.ldq + (int64_t)head * D + 8 * h;
+    const int row = row0 + col, t = row / G;
+    const int head = hk * G + row - t * G;
+    const uint64_t* const words = src.tree + b * src.stride + (int64_t)min(t, nq - 1) * src.words;
+    R r;
+    {
+      const uint16_t* p = a.q + (b * a.Lq + t) * a.ldq + (int64_t)head * D + 8 * h;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      r.q[i] = u32x4{0, 0, 0, 0};
-      if (row < rows) r.q[i] = *reinterpret_cast<const u32x4*>(p + 16 * i);
+      for (int i = 0; i < D / 16; ++i) {
+        r.q[i] = u32x4{0, 0, 0, 0};
+        if (row < rows) r.q[i] = *reinterpret_cast<const u32x4*>(p + 16 * i);
+      }
     }
-  }
 
-  // The table's entries of 64 sixteens of keys, one a lane: those of the 16 tiles
-  // that hold tile t, of the next 16, and of 16 more on their way; named: bit i, the
-  // entry of lane i names a page.
-  const auto entries = [&](int block) {
-    const int64_t first = (int64_t)(base0 >> 4) + 64 * block + lane;
-    const int key = (int)min<int64_t>(16 * first, n - 1);
-    return src.c.table[b * src.c.max_pages + (key >> src.c.page_log2)];
-  };
-  int e0 = 0, e1 = 0, e2 = 0;
-  uint64_t named0 = 0, named1 = 0;
-  const auto look_at = [&] {
-    named0 = __builtin_amdgcn_ballot_w64(src.named(e0));
-    named1 = __builtin_amdgcn_ballot_w64(src.named(e1));
-  };
-  int block = 0;
-  // sixteen s of tile i (within the first two blocks): whether it has a page, and
-  // which (no branches: they would stand among a step's products)
-  const auto has = [&](int i, int s) {
-    const int at = 4 * (i - 16 * block) + s;
-    return (((at < 64 ? named0 : named1) >> (at & 63)) & 1) != 0;
-  };
-  const auto page_of = [&](int i, int s) {
-    const int at = 4 * (i - 16 * block) + s;
-    const int x = __builtin_amdgcn_readlane(e0, at & 63), y = __builtin_amdgcn_readlane(e1, at & 63);
-    return at < 64 ? x : y;
-  };
-  // A thread's units of a tile, 16 elements each: one wave's are consecutive, and from
-  // one sixteen of keys.
-  struct Unit {
-    u32x2 w;
-    uint32_t s;                    // the group scales of its lane and three others'
-  };
-  const auto first_of = [&](int u) { return (u * kTreeThreads + 64 * wave) & (T::kUnits - 1); };
-  int to[T::kPer][2];              // the two pieces' places in a staged tile
-#pragma unroll
-  for (int u = 0; u < T::kPer; ++u)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int y = first_of(u) + lane, key = y / T::kGroups, c = 2 * (y % T::kGroups) + x;
-      to[u][x] = T::is_v(u, wave) ? v_piece<D>(key, c) : k_piece<D>(key, c);
-    }
-  const auto load = [&](Unit& r, int u, int i) {
-    const bool val = T::is_v(u, wave);
-    const int y = first_of(u), s16 = y / T::kGroups >> 4;
-    const int p = page_of(i, s16);
-    const int64_t slot = src.slot(has(i, s16) ? p : 0, hk, base0 + i * kTileKeys + 16 * s16) * T::kGroups + y % (16 * T::kGroups);
-    r.w = *reinterpret_cast<const u32x2*>((val ? src.c.v_q : src.c.k_q) + slot * 8 + 8 * lane);
-    // (a byte's load would be widened, and so waited for, a tile too soon)
-    r.s = *reinterpret_cast<const uint32_t*>((val ? src.c.v_s : src.c.k_s) + slot + (lane & ~3));
-  };
-  // piece x of unit u of tile i into the staged tile `tile` (what has no slot gets a
-  // scale of zero: the bytes may be a NaN's)
-  const auto store = [&](const Unit& r, int u, int x, int i, char* staged) {
-    const int key = first_of(u) / T::kGroups;
-    const int left = has(i, key >> 4) ? n - (base0 + i * kTileKeys) - key : 0;
-    const uint32_t s = min(__builtin_amdgcn_ubfe(r.s, 8 * (lane & 3), 8), T::is_v(u, wave) ? kMostScale : 0xFFu);
-    const f16x2 sc = scale_f16<0>(lane / T::kGroups < left ? s : 0u);
-    *reinterpret_cast<u32x4*>(staged + to[u][x]) = codes_f16(r.w[x], sc);
-  };
-  // group j: K(j + 2) and V(j) (Parts 1: V(j + 1)), loaded two tiles before they are stored
-  const auto of_group = [&](int u, int j) { return j + (T::is_v(u, wave) ? kSooner : 2); };
-  Unit even[T::kPer], odd[T::kPer];
-  if (nt > 0) {
-    e0 = entries(0);
-    e1 = entries(1);
-    e2 = entries(2);
-    look_at();
-    Unit first[T::kPer], second[T::kPer];
-#pragma unroll
-    for (int u = 0; u < T::kPer; ++u) {
-      if (T::is_v(u, wave) && !kSooner) continue;
-      load(first[u], u, 0);
-      if (!T::is_v(u, wave)) load(second[u], u, 1);
-    }
-#pragma unroll
-    for (int u = 0; u < T::kPer; ++u) {
-      load(even[u], u, of_group(u, 0));
-      load(odd[u], u, of_group(u, 1));
-    }
+    // The table's entries of 64 sixteens of keys, one a lane: those of the 16 tiles
+    // that hold tile t, of the next 16, and of 16 more on their way; named: bit i, the
+    // entry of lane i names a page.
+    const auto entries = [&](int block) {
+      const int64_t first = (int64_t)(base0 >> 4) + 64 * block + lane;
+      const int key = (int)min<int64_t>(16 * first, n - 1);
+      return src.c.table[b * src.c.max_pages + (key >> src.c.page_log2)];
+    };
+    int e0 = 0, e1 = 0, e2 = 0;
+    uint64_t named0 = 0, named1 = 0;
+    const auto look_at = [&] {
+      named0 = __builtin_amdgcn_ballot_w64(src.named(e0));
+      named1 = __builtin_amdgcn_ballot_w64(src.named(e1));
+    };
+    int block = 0;
+    // sixteen s of tile i (within the first two blocks): whether it has a page, and
+    // which (no branches: they would stand among a step's products)
+    const auto has = [&](int i, int s) {
+      const int at = 4 * (i - 16 * block) + s;
+      return (((at < 64 ? named0 : named1) >> (at & 63)) & 1) != 0;
+    };
+    const auto page_of = [&](int i, int s) {
+      const int at = 4 * (i - 16 * block) + s;
+      const int x = __builtin_amdgcn_readlane(e0, at & 63), y = __builtin_amdgcn_readlane(e1, at & 63);
+      return at < 64 ? x : y;
+    };
+    // A thread's units of a tile, 16 elements each: one wave's are consecutive, and from
+    // one sixteen of keys.
+    struct Unit {
+      u32x2 w;
+      uint32_t s;                    // the group scales of its lane and three others'
+    };
+    const auto first_of = [&](int u) { return (u * kTreeThreads + 64 * wave) & (T::kUnits - 1); };
+    int to[T::kPer][2];              // the two pieces' places in a staged tile
 #pragma unroll
     for (int u = 0; u < T::kPer; ++u)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        if (T::is_v(u, wave) && !kSooner) continue;
-        store(first[u], u, x, 0, T::is_v(u, wave) ? vt : kt);
-        if (!T::is_v(u, wave)) store(second[u], u, x, 1, kt + kBytes);
+        const int y = first_of(u) + lane, key = y / T::kGroups, c = 2 * (y % T::kGroups) + x;
+        to[u][x] = T::is_v(u, wave) ? v_piece<D>(key, c) : k_piece<D>(key, c);
       }
-  }
-
-  r.c = query_operand<true>(r.q, a.scale * kLog2e, src.k_scale(), [](float v) { return pair_max(v); });
-  r.clear();
-  r.set_ones(lane);
-
-  // this lane's places in a staged tile (attn_tile.hip), in its half of the keys
-  int ka[D / 16], va[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) ka[i] = part * kHalf + k_piece<D>(col, 2 * i + h);
-#pragma unroll
-  for (int d = 0; d < D / 32; ++d)
-    va[d] = kBefore + v_piece<D>(4 * h + ((lane & 15) >> 2), 4 * d + 2 * ((lane >> 4) & 1)) + 8 * (lane & 3);
-
-  f32x16 s0 = {}, s1 = {};
-  u32x4 p0[2] = {}, p1[2] = {};
-  float sum = 0.0f;
-  u32x4 ahead[R::kAhead];
-  if (nt > 0) {
-    __syncthreads();
-    if (mine) {
-      r.logits(s0, kt, ka);
-      if constexpr (Parts == 2)
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) ka[d] += kBytes;
-#pragma unroll
-      for (int g = 0; g < R::kAhead; ++g)
-        ahead[g] = r.template operand<Parts == 1 ? kHalf : 0>(g, kt, ka, vt, va);
-    }
-  }
-  int slot = 0;                                            // t % 3
-  // K(t + 2) and V into their tiles, in `turns` turns
-  const auto store_turn = [&](int turn, int turns, int i, const Unit(&r)[T::kPer]) {
-#pragma unroll
-    for (int j = 0; j < T::kParts; ++j)
-      if (turn == j * turns / T::kParts) {
-        const int u = j / 2;
-        const int k = (slot == 0 ? 2 : slot - 1) * kBytes, v = (!kSooner ? slot : slot == 2 ? 0 : slot + 1) * kBytes;
-        store(r[u], u, j % 2, of_group(u, i), T::is_v(u, wave) ? vt + v : kt + k);
-      }
-  };
-  // the last turns of tile t: the waves meet, group t + 2 is loaded
-  const auto meet_turn = [&](int turn, int i, Unit(&r)[T::kPer]) {
-    if (turn == 4) __syncthreads();
-#pragma unroll
-    for (int u = 0; u < T::kPer; ++u)
-      if (turn == 5 + u) load(r[u], u, of_group(u, i + 2));
-  };
-  const auto turn_over = [&] { slot = slot == 2 ? 0 : slot + 1; };
-  // all tiles in pairs (of the last one's, if it has none, no key is seen), 16 to a
-  // block of entries
-  const auto each = [&](const auto& pair) __attribute__((always_inline)) {
-    for (int i = 0; i < nt;) {
-      for (const int stop = min(nt, 16 * block + 16); i < stop; i += 2) pair(i);
-      ++block;
-      e0 = e1;
-      e1 = e2;
-      e2 = entries(block + 2);
-      look_at();
-    }
-  };
-  // what row `row` sees of tile i's keys, all: all rows see all of them
-  const auto look_up = [&](int i, bool& whole) {
-    const int base = base0 + i * kTileKeys;
-    // (bit t of 4: sixteen t of the tile)
-    const uint32_t ok = (uint32_t)(named0 >> (4 * (i & 15))) & 15u;
-    uint64_t here = ~0ull;
-    if (ok != 15u) {
-      here = 0;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) here |= (ok >> x) & 1 ? 0xFFFFull << (16 * x) : 0;
-    }
-    const int left = min(n, base0 + nt * kTileKeys) - base;
-    if (left < kTileKeys) here = left <= 0 ? 0 : here & ((1ull << left) - 1);
-    whole = here == ~0ull && base + kTileKeys <= all;
-    return whole ? here : here & src.row_sees(words, base, all);
-  };
-  // Tile i.  Parts 2: `s` its logits, `next` the logits of the tile before (whose
-  // weights are p); Parts 1: the same of its first half and the half before.
-  const auto tile_of = [&](int i, f32x16& s, u32x4(&pn)[2], f32x16& next, u32x4(&p)[2], Unit(&units)[T::kPer]) __attribute__((always_inline)) {
-    bool whole;
-    const uint64_t here = look_up(i, whole);
-    if constexpr (Parts == 2) {
-      if (!whole) hide(s, (uint32_t)(here >> (32 * part)), 64, h);
-      // on to K(t + 2) and V(t)
-      const int ks = slot == 1 ? -2 * kBytes : kBytes;
-      const int vs = i == 0 ? part * kHalf - kBefore : slot == 0 ? -2 * kBytes : kBytes;
-      r.template step<0, 0>(s, pn, next, p, sum, ahead, kt, ka, vt, va, ks, vs, [&](int turn) {
-        if (turn < 4)
-          store_turn(turn, 4, i, units);
-        else
-          meet_turn(turn, i, units);
-      });
-    } else {
-      if (!whole) hide(s, (uint32_t)here, 64, h);
-      // on to K(t + 1) and V(t)
-      const int ks = slot == 2 ? -2 * kBytes : kBytes;
-      const int vs = i == 0 ? -kBefore : slot == 0 ? -2 * kBytes : kBytes;
-      r.template step<kHalf, 0>(s, pn, next, p, sum, ahead, kt, ka, vt, va, ks, vs,
-                                [&](int turn) { store_turn(turn - 1, 6, i, units); });
-      if (!whole) hide(next, (uint32_t)(here >> 32), 64, h);
-      r.template step<0, kHalf>(next, p, s, pn, sum, ahead, kt, ka, vt, va, 0, 0,
-                                [&](int turn) { meet_turn(turn, i, units); });
-    }
-    turn_over();
-  };
-  if (mine) {
-    each([&](int i) {
-      tile_of(i, s0, p0, s1, p1, even);
-      if constexpr (Parts == 2)
-        tile_of(i + 1, s1, p1, s0, p0, odd);
-      else
-        tile_of(i + 1, s0, p0, s1, p1, odd);
-    });
-    if (nt > 0) r.template second<Parts == 1 ? kHalf : 0>(s1, p1, sum, vt, va);
-  } else {
-    const auto pass = [&](int i, Unit(&units)[T::kPer]) {
-#pragma unroll
-      for (int turn = 0; turn < 4; ++turn) store_turn(turn, 4, i, units);
-#pragma unroll
-      for (int turn = 4; turn < 8; ++turn) meet_turn(turn, i, units);
-      turn_over();
+    const auto load = [&](Unit& r, int u, int i) {
+      const bool val = T::is_v(u, wave);
+      const int y = first_of(u), s16 = y / T::kGroups >> 4;
+      const int p = page_of(i, s16);
+      const int64_t first = src.slot(has(i, s16) ? p : 0, hk, base0 + i * kTileKeys + 16 * s16);
+      const int64_t slot = first * T::kGroups + y % (16 * T::kGroups);
+      r.w = *reinterpret_cast<const u32x2*>((val ? src.c.v_q : src.c.k_q) + slot * 8 + 8 * lane);
+      // (a byte's load would be widened, and so waited for, a tile too soon)
+      r.s = *reinterpret_cast<const uint32_t*>((val ? src.c.v_s : src.c.k_s) + slot + (lane & ~3));
     };
-    each([&](int i) {
-      pass(i, even);
-      pass(i + 1, odd);
-    });
-  }
-
-  // the other half's sums to the common reference
-  __syncthreads();
-  if constexpr (Parts == 2) {
-    float* const join = reinterpret_cast<float*>(lds + group * kJoin) + col * (D + 4);
-    if (part == 1) {
-      if (h == 0) {
-        ml[0][group][col] = r.m;
-        ml[1][group][col] = r.l;
+    // piece x of unit u of tile i into the staged tile `tile` (what has no slot gets a
+    // scale of zero: the bytes may be a NaN's)
+    const auto store = [&](const Unit& r, int u, int x, int i, char* staged) {
+      const int key = first_of(u) / T::kGroups;
+      const int left = has(i, key >> 4) ? n - (base0 + i * kTileKeys) - key : 0;
+      const uint32_t s = min(__builtin_amdgcn_ubfe(r.s, 8 * (lane & 3), 8), T::is_v(u, wave) ? kMostScale : 0xFFu);
+      const f16x2 sc = scale_f16<0>(lane / T::kGroups < left ? s : 0u);
+      *reinterpret_cast<u32x4*>(staged + to[u][x]) = codes_f16(r.w[x], sc);
+    };
+    // group j: K(j + 2) and V(j) (Parts 1: V(j + 1)), loaded two tiles before they are stored
+    const auto of_group = [&](int u, int j) { return j + (T::is_v(u, wave) ? kSooner : 2); };
+    Unit even[T::kPer], odd[T::kPer];
+    if (nt > 0) {
+      e0 = entries(0);
+      e1 = entries(1);
+      e2 = entries(2);
+      look_at();
+      Unit first[T::kPer], second[T::kPer];
+#pragma unroll
+      for (int u = 0; u < T::kPer; ++u) {
+        if (T::is_v(u, wave) && !kSooner) continue;
+        load(first[u], u, 0);
+        if (!T::is_v(u, wave)) load(second[u], u, 1);
       }
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d)
+      for (int u = 0; u < T::kPer; ++u) {
+        load(even[u], u, of_group(u, 0));
+        load(odd[u], u, of_group(u, 1));
+      }
 #pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<f32x4*>(join + 32 * d + 2 * i + 4 * h) =
-              f32x4{r.o[d][i], r.o[d][i + 1], r.o[d][i + 2], r.o[d][i + 3]};
-    }
-    __syncthreads();
-    if (part == 0) {
-      const float m1 = ml[0][group][col], top = fmaxf(r.m, m1), ref = top == -INFINITY ? 0.0f : top;
-      // (times zero, not left out: a sum that is NaN stays so)
-      const float f0 = r.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((r.m - ref) * r.c);
-      const float f1 = m1 == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m1 - ref) * r.c);
-      r.m = top;
-      r.l = __builtin_fmaf(ml[1][group][col], f1, r.l * f0);
+      for (int u = 0; u < T::kPer; ++u)
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const f32x4 o = *reinterpret_cast<const f32x4*>(join + 32 * d + 2 * i + 4 * h);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) r.o[d][i + j] = __builtin_fmaf(o[j], f1, r.o[d][i + j] * f0);
+        for (int x = 0; x < 2; ++x) {
+          if (T::is_v(u, wave) && !kSooner) continue;
+          store(first[u], u, x, 0, T::is_v(u, wave) ? vt : kt);
+          if (!T::is_v(u, wave)) store(second[u], u, x, 1, kt + kBytes);
         }
     }
-    __syncthreads();
-  }
-  if (part == 0) {
-    if (sp.shares ? c1 - c0 == len : sp.pieces == 1) {
-      store_rows(r, src.v_scale(), a.o + (b * a.Lq + t) * a.ldo + (int64_t)head * D, h, row < rows);
-    } else if (row < rows) {
-      const int64_t to = (int64_t)((int)blockIdx.x + (sp.shares && c0 == 0 ? sp.shares + (sp.by_unit ? unit - (int)blockIdx.x : 0) : 0)) * kRows + group * 32 + col;
+
+    r.c = query_operand<true>(r.q, a.scale * kLog2e, src.k_scale(), [](float v) { return pair_max(v); });
+    r.clear();
+    r.set_ones(lane);
+
+    // this lane's places in a staged tile (attn_tile.hip), in its half of the keys
+    int ka[D / 16], va[D / 32];
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d)
+    for (int i = 0; i < D / 16; ++i) ka[i] = part * kHalf + k_piece<D>(col, 2 * i + h);
 #pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<f32x4*>(sp.o + to * D + 32 * d + 2 * i + 4 * h) =
-              f32x4{r.o[d][i], r.o[d][i + 1], r.o[d][i + 2], r.o[d][i + 3]};
-      if (h == 0) {
-        sp.m[to] = r.m == -INFINITY ? r.m : r.m * r.c;
-        sp.l[to] = r.l;
+    for (int d = 0; d < D / 32; ++d)
+      va[d] = kBefore + v_piece<D>(4 * h + ((lane & 15) >> 2), 4 * d + 2 * ((lane >> 4) & 1)) + 8 * (lane & 3);
+
+    f32x16 s0 = {}, s1 = {};
+    u32x4 p0[2] = {}, p1[2] = {};
+    float sum = 0.0f;
+    u32x4 ahead[R::kAhead];
+    if (nt > 0) {
+      __syncthreads();
+      if (mine) {
+        r.logits(s0, kt, ka);
+        if constexpr (Parts == 2)
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) ka[d] += kBytes;
+#pragma unroll
+        for (int g = 0; g < R::kAhead; ++g)
+          ahead[g] = r.template operand<Parts == 1 ? kHalf : 0>(g, kt, ka, vt, va);
       }
     }
-  }
-  // on to the next unit
-  at += c1 - c0;
-  if (at >= stop) return;
-  c0 = 0;
-  if (++tile == tree_tiles(nq, G, kRows)) {
-    tile = 0;
-    if (++hk == a.Hkv) {
-      hk = 0;
-      do nq = src.queries(++b, a.Lq);
-      while (nq == 0);
-      n = src.keys(b);
+    int slot = 0;                                            // t % 3
+    // K(t + 2) and V into their tiles, in `turns` turns
+    const auto store_turn = [&](int turn, int turns, int i, const Unit(&r)[T::kPer]) {
+#pragma unroll
+      for (int j = 0; j < T::kParts; ++j)
+        if (turn == j * turns / T::kParts) {
+          const int u = j / 2;
+          const int k = (slot == 0 ? 2 : slot - 1) * kBytes, v = (!kSooner ? slot : slot == 2 ? 0 : slot + 1) * kBytes;
+          store(r[u], u, j % 2, of_group(u, i), T::is_v(u, wave) ? vt + v : kt + k);
+        }
+    };
+    // the last turns of tile t: the waves meet, group t + 2 is loaded
+    const auto meet_turn = [&](int turn, int i, Unit(&r)[T::kPer]) {
+      if (turn == 4) __syncthreads();
+#pragma unroll
+      for (int u = 0; u < T::kPer; ++u)
+        if (turn == 5 + u) load(r[u], u, of_group(u, i + 2));
+    };
+    const auto turn_over = [&] { slot = slot == 2 ? 0 : slot + 1; };
+    // all tiles in pairs (of the last one's, if it has none, no key is seen), 16 to a
+    // block of entries
+    const auto each = [&](const auto& pair) __attribute__((always_inline)) {
+      for (int i = 0; i < nt;) {
+        for (const int stop = min(nt, 16 * block + 16); i < stop; i += 2) pair(i);
+        ++block;
+        e0 = e1;
+        e1 = e2;
+        e2 = entries(block + 2);
+        look_at();
+      }
+    };
+    // what row `row` sees of tile i's keys, all: all rows see all of them
+    const auto look_up = [&](int i, bool& whole) {
+      const int base = base0 + i * kTileKeys;
+      // (bit t of 4: sixteen t of the tile)
+      const uint32_t ok = (uint32_t)(named0 >> (4 * (i & 15))) & 15u;
+      uint64_t here = ~0ull;
+      if (ok != 15u) {
+        here = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) here |= (ok >> x) & 1 ? 0xFFFFull << (16 * x) : 0;
+      }
+      const int left = min(n, base0 + nt * kTileKeys) - base;
+      if (left < kTileKeys) here = left <= 0 ? 0 : here & ((1ull << left) - 1);
+      whole = here == ~0ull && base + kTileKeys <= all;
+      return whole ? here : here & src.row_sees(words, base, all);
+    };
+    // Tile i.  Parts 2: `s` its logits, `next` the logits of the tile before (whose
+    // weights are p); Parts 1: the same of its first half and the half before.
+    const auto tile_of = [&](int i, f32x16& s, u32x4(&pn)[2], f32x16& next, u32x4(&p)[2],
+                             Unit(&units)[T::kPer]) __attribute__((always_inline)) {
+      bool whole;
+      const uint64_t here = look_up(i, whole);
+      if constexpr (Parts == 2) {
+        if (!whole) hide(s, (uint32_t)(here >> (32 * part)), 64, h);
+        // on to K(t + 2) and V(t)
+        const int ks = slot == 1 ? -2 * kBytes : kBytes;
+        const int vs = i == 0 ? part * kHalf - kBefore : slot == 0 ? -2 * kBytes : kBytes;
+        r.template step<0, 0>(s, pn, next, p, sum, ahead, kt, ka, vt, va, ks, vs, [&](int turn) {
+          if (turn < 4)
+            store_turn(turn, 4, i, units);
+          else
+            meet_turn(turn, i, units);
+        });
+      } else {
+        if (!whole) hide(s, (uint32_t)here, 64, h);
+        // on to K(t + 1) and V(t)
+        const int ks = slot == 2 ? -2 * kBytes : kBytes;
+        const int vs = i == 0 ? -kBefore : slot == 0 ? -2 * kBytes : kBytes;
+        r.template step<kHalf, 0>(s, pn, next, p, sum, ahead, kt, ka, vt, va, ks, vs,
+                                  [&](int turn) { store_turn(turn - 1, 6, i, units); });
+        if (!whole) hide(next, (uint32_t)(here >> 32), 64, h);
+        r.template step<0, kHalf>(next, p, s, pn, sum, ahead, kt, ka, vt, va, 0, 0,
+                                  [&](int turn) { meet_turn(turn, i, units); });
+      }
+      turn_over();
+    };
+    if (mine) {
+      each([&](int i) {
+        tile_of(i, s0, p0, s1, p1, even);
+        if constexpr (Parts == 2)
+          tile_of(i + 1, s1, p1, s0, p0, odd);
+        else
+          tile_of(i + 1, s0, p0, s1, p1, odd);
+      });
+      if (nt > 0) r.template second<Parts == 1 ? kHalf : 0>(s1, p1, sum, vt, va);
+    } else {
+      const auto pass = [&](int i, Unit(&units)[T::kPer]) {
+#pragma unroll
+        for (int turn = 0; turn < 4; ++turn) store_turn(turn, 4, i, units);
+#pragma unroll
+        for (int turn = 4; turn < 8; ++turn) meet_turn(turn, i, units);
+        turn_over();
+      };
+      each([&](int i) {
+        pass(i, even);
+        pass(i + 1, odd);
+      });
     }
-  }
+
+    // the other half's sums to the common reference
+    __syncthreads();
+    if constexpr (Parts == 2) {
+      float* const join = reinterpret_cast<float*>(lds + group * kJoin) + col * (D + 4);
+      if (part == 1) {
+        if (h == 0) {
+          ml[0][group][col] = r.m;
+          ml[1][group][col] = r.l;
+        }
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<f32x4*>(join + 32 * d + 2 * i + 4 * h) =
+                f32x4{r.o[d][i], r.o[d][i + 1], r.o[d][i + 2], r.o[d][i + 3]};
+      }
+      __syncthreads();
+      if (part == 0) {
+        const float m1 = ml[0][group][col], top = fmaxf(r.m, m1), ref = top == -INFINITY ? 0.0f : top;
+        // (times zero, not left out: a sum that is NaN stays so)
+        const float f0 = r.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((r.m - ref) * r.c);
+        const float f1 = m1 == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m1 - ref) * r.c);
+        r.m = top;
+        r.l = __builtin_fmaf(ml[1][group][col], f1, r.l * f0);
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const f32x4 o = *reinterpret_cast<const f32x4*>(join + 32 * d + 2 * i + 4 * h);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r.o[d][i + j] = __builtin_fmaf(o[j], f1, r.o[d][i + j] * f0);
+          }
+      }
+      __syncthreads();
+    }
+    if (part == 0) {
+      if (sp.shares ? c1 - c0 == len : sp.pieces == 1) {
+        store_rows(r, src.v_scale(), a.o + (b * a.Lq + t) * a.ldo + (int64_t)head * D, h, row < rows);
+      } else if (row < rows) {
+        int sum = blockIdx.x;
+        if (sp.shares && c0 == 0) sum = sp.shares + (sp.by_unit ? unit : sum);
+        const int64_t to = (int64_t)sum * kRows + group * 32 + col;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<f32x4*>(sp.o + to * D + 32 * d + 2 * i + 4 * h) =
+                f32x4{r.o[d][i], r.o[d][i + 1], r.o[d][i + 2], r.o[d][i + 3]};
+        if (h == 0) {
+          sp.m[to] = r.m == -INFINITY ? r.m : r.m * r.c;
+          sp.l[to] = r.l;
+        }
+      }
+    }
+    // on to the next unit
+    at += c1 - c0;
+    if (at >= stop) return;
+    c0 = 0;
+    if (++tile == tree_tiles(nq, G, kRows)) {
+      tile = 0;
+      if (++hk == a.Hkv) {
+        hk = 0;
+        do nq = src.queries(++b, a.Lq);
+        while (nq == 0);
+        n = src.keys(b);
+      }
+    }
   }
 }
 
@@ -599,7 +603,8 @@ TreeCut tree_cut(int64_t B, int64_t units, int rows, int D, int parts, int64_t l
     const int64_t sums = shares + (units < shares ? units : shares);
     if (TreeSums::bytes(sums, units, rows, D) > ws_bytes) continue;
     const double per = (double)units / shares;
-    const double t = kListTime * (double)((B + 63) / 64) + per * (double)len * each + (1.0 + per) * kUnitStart + tree_join_time(sums, rows, D);
+    const double t = kListTime * (double)((B + 63) / 64) + per * (double)len * each + (1.0 + per) * kUnitStart +
+                     tree_join_time(sums, rows, D);
     if (t < 1.1 * least) take(shares, 0, sums);
     break;
   }
