@@ -574,7 +574,10 @@ int attn_kv4(const uint16_t* q, int64_t ldq, int64_t B, int64_t Lq, int Hq, int 
  * aligned; tree_stride in words, at least Lq W, or 0: one tree for all streams).
  * Bits of tokens from q_lens[b] on are ignored; a row that sees nothing gives
  * zeros; what a token holds that a row does not see changes nothing of that row
- * (NaN's scales included).  Lq <= 1024.  Everything else, the workspace too, as for attn_kv4.
+ * (NaN's scales included).  Group scales that append does not write, as attn_kv4
+ * reads them: a negative one is that number, and one of values that is NaN makes NaN
+ * of its 16 elements in every row that sees the token.  Lq <= 1024.  Everything else,
+ * the workspace too, as for attn_kv4.
  *
  * kv4_keep: the tokens of a checked tree that are kept move to the front of the
  * drafted positions: the codes and scales of position start[b] + path[b T + i]

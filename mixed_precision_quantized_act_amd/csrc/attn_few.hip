@@ -145,9 +145,10 @@ struct Few<Kv4Source, D, Once> {
     return D == 128 ? (key >> 2) & 3 : (key >> 3) & 1;
   }
   // Tree: a drafted token that some rows do not see may have a NaN's scale, and its
-  // weight of zero needs a number (act_quant's are at most 448).
-  template <bool Tree>
-  static __device__ __forceinline__ void stage_v(const Regs& r, char* lds, int lane) {
+  // weight of zero needs a number.  Where the rows may see different keys (`apart`) such a
+  // group is staged as zeros, and odd(group, keys) is told of it.
+  template <bool Tree, class Odd>
+  static __device__ __forceinline__ void stage_v(const Regs& r, char* lds, int lane, bool apart, const Odd& odd) {
 #pragma unroll
     for (int u = 0; u < kVLoads; ++u) {
       const int x = u * 64 + lane, vk = x / (D / 32), c = x % (D / 32);
@@ -157,18 +158,20 @@ struct Few<Kv4Source, D, Once> {
     const bool on = (r.seen >> lane) & 1;      // (bytes of slots that are not seen may be NaN codes)
 #pragma unroll
     for (int i = 0; i < kGroups / 4; ++i) {
-      f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)r.vs[i], false);
-      f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8((int)r.vs[i], true);
+      const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)r.vs[i], false);
+      const f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8((int)r.vs[i], true);
+      float f[4] = {on ? a[0] : 0.0f, on ? a[1] : 0.0f, on ? b[0] : 0.0f, on ? b[1] : 0.0f};
       if constexpr (Tree)
+        if (apart) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          a[j] = fminf(a[j], 448.0f);
-          b[j] = fminf(b[j], 448.0f);
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t keys = __builtin_amdgcn_ballot_w64(__builtin_isnan(f[j]));
+            if (keys) odd(4 * i + j, keys);
+            f[j] = __builtin_isnan(f[j]) ? 0.0f : f[j];
+          }
         }
-      sc[(4 * i + 0) * kFewKeys + lane] = (_Float16)(on ? a[0] : 0.0f);
-      sc[(4 * i + 1) * kFewKeys + lane] = (_Float16)(on ? a[1] : 0.0f);
-      sc[(4 * i + 2) * kFewKeys + lane] = (_Float16)(on ? b[0] : 0.0f);
-      sc[(4 * i + 3) * kFewKeys + lane] = (_Float16)(on ? b[1] : 0.0f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sc[(4 * i + j) * kFewKeys + lane] = (_Float16)f[j];
     }
   }
   // V^T of elements 16 d .. 16 d + 15: lane (element, g), keys 16 t + 4 g + 0..3,
@@ -237,8 +240,8 @@ struct Few<CrossSource, D, Once> {
   static __device__ __forceinline__ int swizzle(int key) {
     return D == 128 ? key & 7 : (key >> 1) & 3;
   }
-  template <bool>
-  static __device__ __forceinline__ void stage_v(const Regs& r, char* lds, int lane) {
+  template <bool, class Odd>
+  static __device__ __forceinline__ void stage_v(const Regs& r, char* lds, int lane, bool, const Odd&) {
 #pragma unroll
     for (int u = 0; u < kVLoads; ++u) {
       const int x = u * 64 + lane, vk = x / (D / 8), c = x % (D / 8);
@@ -350,14 +353,21 @@ attn_few_kernel(AttnArgs a, Source src, AttnSplit sp, int tiles, int splits, Gat
         for (int i = 0; i < D / 32; ++i) s[x][t4] = mfma16<kF16>(k[i], q[x][i], s[x][t4]);
       }
     }
-    F::template stage_v<Source::kTree>(cur, vlds, lane);
     const uint64_t seen = cur.seen;
+    const bool whole = seen == ~0ull && base + kFewKeys <= all;
+    // (o[x][d] is group d: NaN for the rows that see one of the keys, whatever is added)
+    F::template stage_v<Source::kTree>(cur, vlds, lane, !whole, [&](int d, uint64_t keys) {
+      if constexpr (Source::kTree)
+#pragma unroll
+        for (int x = 0; x < Sets; ++x)
+          if (keys & src.row_sees(words[x], base, all))
+            o[x][d] = f32x4{__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
+    });
     // the next step's loads, and what those of the one after need
     if (ch + kFewWaves < c1) {
       F::load(cur, src, look, b, hk, base + kFewWaves * kFewKeys, n, lane);
       look = src.look(b, base + 2 * kFewWaves * kFewKeys, n, lane);
     }
-    const bool whole = seen == ~0ull && base + kFewKeys <= all;
     if (!whole) {
 #pragma unroll
       for (int x = 0; x < Sets; ++x) {

@@ -29,10 +29,6 @@ namespace {
 constexpr int kTreeWaves = 8, kTreeThreads = 64 * kTreeWaves;
 constexpr int tree_rows(int parts) { return 32 * kTreeWaves / parts; }
 
-// The largest scale of values: a NaN's bits may stand in a drafted token's that some
-// rows do not see, whose weight of zero needs a number (no scale is negative).
-constexpr uint32_t kMostScale = 0x7E;
-
 // Sums of a part of the keys.  Shares of the list: share w's own are of a unit that began
 // in an earlier one; behind all shares' stand those of a unit that goes on in the next
 // (of unit u at u, or with more units than shares at w).  Equal pieces: one each, unit
@@ -134,6 +130,7 @@ attn_tree_kernel(AttnArgs a, Kv4TreeSource src, TreeSums sp, int tiles, Gate gat
   static_assert(kLds >= 4 * kJoin, "the waves' sums");
   __shared__ __align__(16) char lds[kLds];
   __shared__ float ml[2][4][32];
+  __shared__ int nan_unit;         // the last unit (from 1) with a NaN among its values' scales
   char* const kt = lds;
   char* const vt = lds + 3 * kBytes;
 
@@ -145,6 +142,7 @@ attn_tree_kernel(AttnArgs a, Kv4TreeSource src, TreeSums sp, int tiles, Gate gat
   if (wave >= kTreeWaves / 2) __builtin_amdgcn_s_setprio(1);
 
   if (tid < kHalf / 16) *reinterpret_cast<u32x4*>(vt + 3 * kBytes + 16 * tid) = u32x4{0, 0, 0, 0};
+  if (tid == 0) nan_unit = 0;
 
   int at = 0, stop = 1;
   int64_t b = 0;
@@ -176,7 +174,7 @@ attn_tree_kernel(AttnArgs a, Kv4TreeSource src, TreeSums sp, int tiles, Gate gat
     c0 = at = (int)((int64_t)len * piece / sp.pieces);
     stop = (int)((int64_t)len * (piece + 1) / sp.pieces);
   }
-  for (;;) {
+  for (int taken = 1;; ++taken) {
     // (a new value each time: the places that follow from it would be kept in registers
     // beside a unit's, and those of 128 spill)
     int lane = tid & 63;
@@ -257,13 +255,20 @@ attn_tree_kernel(AttnArgs a, Kv4TreeSource src, TreeSums sp, int tiles, Gate gat
       r.s = *reinterpret_cast<const uint32_t*>((val ? src.c.v_s : src.c.k_s) + slot + (lane & ~3));
     };
     // piece x of unit u of tile i into the staged tile `tile` (what has no slot gets a
-    // scale of zero: the bytes may be a NaN's)
+    // scale of zero: the bytes may be a NaN's).  A NaN's scale may also stand in a drafted
+    // token's that some rows do not see, whose weight of zero needs a number: among
+    // values it counts as 448 here, and `nans`, a sum of zeros, tells of it.
+    float nans = 0.0f;
     const auto store = [&](const Unit& r, int u, int x, int i, char* staged) {
       const int key = first_of(u) / T::kGroups;
       const int left = has(i, key >> 4) ? n - (base0 + i * kTileKeys) - key : 0;
-      const uint32_t s = min(__builtin_amdgcn_ubfe(r.s, 8 * (lane & 3), 8), T::is_v(u, wave) ? kMostScale : 0xFFu);
-      const f16x2 sc = scale_f16<0>(lane / T::kGroups < left ? s : 0u);
-      *reinterpret_cast<u32x4*>(staged + to[u][x]) = codes_f16(r.w[x], sc);
+      const uint32_t s = __builtin_amdgcn_ubfe(r.s, 8 * (lane & 3), 8);
+      float f = __builtin_amdgcn_cvt_f32_fp8((int)(lane / T::kGroups < left ? s : 0u), 0);
+      if (T::is_v(u, wave)) {
+        if (x == 0) nans = __builtin_fmaf(f, 0.0f, nans);
+        f = fminf(f, 448.0f);
+      }
+      *reinterpret_cast<u32x4*>(staged + to[u][x]) = codes_f16(r.w[x], f16x2{(_Float16)f, (_Float16)f});
     };
     // group j: K(j + 2) and V(j) (Parts 1: V(j + 1)), loaded two tiles before they are stored
     const auto of_group = [&](int u, int j) { return j + (T::is_v(u, wave) ? kSooner : 2); };
@@ -423,8 +428,9 @@ attn_tree_kernel(AttnArgs a, Kv4TreeSource src, TreeSums sp, int tiles, Gate gat
       });
     }
 
-    // the other half's sums to the common reference
+    if (nans != nans) nan_unit = taken;
     __syncthreads();
+    // the other half's sums to the common reference
     if constexpr (Parts == 2) {
       float* const join = reinterpret_cast<float*>(lds + group * kJoin) + col * (D + 4);
       if (part == 1) {
@@ -459,12 +465,14 @@ attn_tree_kernel(AttnArgs a, Kv4TreeSource src, TreeSums sp, int tiles, Gate gat
       __syncthreads();
     }
     if (part == 0) {
-      if (sp.shares ? c1 - c0 == len : sp.pieces == 1) {
-        store_rows(r, src.v_scale(), a.o + (b * a.Lq + t) * a.ldo + (int64_t)head * D, h, row < rows);
+      const bool done = sp.shares ? c1 - c0 == len : sp.pieces == 1;
+      uint16_t* const out = a.o + (b * a.Lq + t) * a.ldo + (int64_t)head * D;
+      int sum = blockIdx.x;
+      if (sp.shares && c0 == 0) sum = sp.shares + (sp.by_unit ? unit : sum);
+      const int64_t to = (int64_t)sum * kRows + group * 32 + col;
+      if (done) {
+        store_rows(r, src.v_scale(), out, h, row < rows);
       } else if (row < rows) {
-        int sum = blockIdx.x;
-        if (sp.shares && c0 == 0) sum = sp.shares + (sp.by_unit ? unit : sum);
-        const int64_t to = (int64_t)sum * kRows + group * 32 + col;
 #pragma unroll
         for (int d = 0; d < D / 32; ++d)
 #pragma unroll
@@ -474,6 +482,31 @@ attn_tree_kernel(AttnArgs a, Kv4TreeSource src, TreeSums sp, int tiles, Gate gat
         if (h == 0) {
           sp.m[to] = r.m == -INFINITY ? r.m : r.m * r.c;
           sp.l[to] = r.l;
+        }
+      }
+      // What the products left out: a row that sees a key with a NaN's scale has NaN in
+      // that group's elements, over what this wave has just stored there.  (Hardly ever:
+      // kv4_append writes no NaN.)
+      if (__builtin_expect(nan_unit == taken, 0)) {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+#pragma unroll 1
+        for (int i = 0; i < nt; ++i) {
+          const int base = base0 + i * kTileKeys, key = base + lane;
+          const int e = src.c.table[b * src.c.max_pages + (min(key, n - 1) >> src.c.page_log2)];
+          const bool there = src.named(e) && key < n;
+          const uint8_t* const s = src.c.v_s + src.slot(there ? e : 0, hk, key) * (D / 16);
+          const uint64_t sees = src.row_sees(words, base, all);
+#pragma unroll 1
+          for (int g = 0; g < D / 16; ++g) {
+            const uint64_t nan = __builtin_amdgcn_ballot_w64(there && (s[g] & 0x7F) == 0x7F);
+            if ((nan & sees) && row < rows) {
+              const uint32_t x = done ? 0x7FC07FC0u : 0x7FC00000u;
+              u32x4* const p = done ? reinterpret_cast<u32x4*>(out + 16 * g + 8 * h)
+                                    : reinterpret_cast<u32x4*>(sp.o + to * D + 16 * g + 8 * h);
+              p[0] = u32x4{x, x, x, x};
+              if (!done) p[1] = u32x4{x, x, x, x};
+            }
+          }
         }
       }
     }
