@@ -38,16 +38,19 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // Position of 16-byte piece c of key `key` in a staged tile (bytes).  K is
 // read as 16-byte pieces of 32 keys, V as 32-byte pieces of 8 keys; the
-// exchange among a key's pieces spreads either over all banks.  (V of 128: two
-// pieces of four keys are read at once, so keys 4 k .. 4 k + 3 differ in the exchange's
-// upper bits; by key % 8 they would meet, 291 against 283 us for 128 rows of a tree.)
+// exchange among a key's pieces spreads either over all banks.
 template <int D>
 __device__ __forceinline__ int k_piece(int key, int c) {
   return key * (D * 2) + 16 * (c ^ (D == 128 ? key & 15 : (key >> 1) & 7));
 }
-template <int D>
+// Spread: two pieces of four keys of 128 are read at once, so keys 4 k .. 4 k + 3 differ in
+// the exchange's upper bits; by key % 8 they meet.  A tree's 128 rows, waves on half a
+// tile each: 291 -> 283 us; the tiles of other queries, all waves on the whole tile: 1350 rows,
+// 16 heads, 12376 keys 170.8 -> 172.8, causal 171.6 -> 171.2, to bf16 states no change.
+template <int D, bool Spread = false>
 __device__ __forceinline__ int v_piece(int key, int c) {
-  return key * (D * 2) + 32 * ((c >> 1) ^ (D == 128 ? 2 * (key & 3) + ((key >> 2) & 1) : key & 3)) + 16 * (c & 1);
+  const int by = D != 128 ? key & 3 : Spread ? 2 * (key & 3) + ((key >> 2) & 1) : key & 7;
+  return key * (D * 2) + 32 * ((c >> 1) ^ by) + 16 * (c & 1);
 }
 
 // Before a row has seen a key: any logit plus this gives an infinite weight,

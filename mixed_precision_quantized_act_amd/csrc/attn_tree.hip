@@ -242,7 +242,7 @@ attn_tree_kernel(AttnArgs a, Kv4TreeSource src, TreeSums sp, int tiles, Gate gat
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int y = first_of(u) + lane, key = y / T::kGroups, c = 2 * (y % T::kGroups) + x;
-        to[u][x] = T::is_v(u, wave) ? v_piece<D>(key, c) : k_piece<D>(key, c);
+        to[u][x] = T::is_v(u, wave) ? v_piece<D, true>(key, c) : k_piece<D>(key, c);
       }
     const auto load = [&](Unit& r, int u, int i) {
       const bool val = T::is_v(u, wave);
@@ -310,7 +310,7 @@ attn_tree_kernel(AttnArgs a, Kv4TreeSource src, TreeSums sp, int tiles, Gate gat
     for (int i = 0; i < D / 16; ++i) ka[i] = part * kHalf + k_piece<D>(col, 2 * i + h);
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
-      va[d] = kBefore + v_piece<D>(4 * h + ((lane & 15) >> 2), 4 * d + 2 * ((lane >> 4) & 1)) + 8 * (lane & 3);
+      va[d] = kBefore + v_piece<D, true>(4 * h + ((lane & 15) >> 2), 4 * d + 2 * ((lane >> 4) & 1)) + 8 * (lane & 3);
 
     f32x16 s0 = {}, s1 = {};
     u32x4 p0[2] = {}, p1[2] = {};
