@@ -28,7 +28,7 @@ hipError_t launch(const AttnArgs& a, const Source& src, int64_t L, void* ws, siz
 
 size_t attn_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
   if (many(Lq, Hq, Hkv)) return attn_tile_ws_bytes(B, Lq, Hq, Hkv, D, L);
-  return attn_few_ws_bytes(B, Lq, Hq, Hkv, D, L);
+  return attn_few_ws_bytes(false, B, Lq, Hq, Hkv, D, L);
 }
 
 size_t attn_cross_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t Lk) {
@@ -59,7 +59,7 @@ bool tree_few(int64_t B, int64_t Lq, int Hq, int Hkv, int64_t L) {
 }  // namespace
 
 size_t attn_kv4_tree_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
-  return tree_few(B, Lq, Hq, Hkv, L) ? attn_few_ws_bytes(B, Lq, Hq, Hkv, D, L)
+  return tree_few(B, Lq, Hq, Hkv, L) ? attn_few_ws_bytes(true, B, Lq, Hq, Hkv, D, L)
                                      : attn_tree_ws_bytes(B, Lq, Hq, Hkv, D, L);
 }
 

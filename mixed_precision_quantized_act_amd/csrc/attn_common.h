@@ -312,8 +312,8 @@ struct AttnSplit {
 };
 
 // Few query rows, the keys split over workgroups (attn_few.hip); L: the most
-// keys a stream can have.
-size_t attn_few_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L);
+// keys a stream can have; tree: of a tree's call.
+size_t attn_few_ws_bytes(bool tree, int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L);
 template <class Source>
 hipError_t launch_attn_few(const AttnArgs& a, const Source& src, int64_t L, void* ws,
                            size_t ws_bytes, hipStream_t stream);

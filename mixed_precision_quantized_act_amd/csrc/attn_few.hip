@@ -21,14 +21,11 @@
 #include <type_traits>
 
 #include "attn_common.h"
+#include "attn_few_plan.h"
 
 namespace qact {
 
 namespace {
-
-constexpr int kFewKeys = 64;     // keys of a wave's step
-constexpr int kFewRows = 16;     // rows of a tile
-constexpr int kFewWaves = 4;
 
 typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -544,58 +541,20 @@ attn_join_kernel(AttnArgs a, Source src, AttnSplit sp, int splits, Gate gate) {
       u32x2{bf16_pack(o[0] * f, o[1] * f), bf16_pack(o[2] * f, o[3] * f)};
 }
 
-// Workgroups to aim for: a few for each of the 256 compute units, so that
-// streams of different lengths even out (16 streams of up to 32768 tokens, 8
-// heads of 128: 256 143 us, 512 109, 1024 105, 2048 110).  Of bf16 heads of 128
-// one workgroup runs at a time on a unit, and each round waits for its first
-// keys: one round (16 tokens to 4000 states, 8 heads: 1024 69 us, 512 60, 256 56, 262
-// MB at 4.7 TB/s).
-constexpr int64_t kFewBlocks = 1024, kFewBlocksWide = 256;
-
-int64_t tiles_of(int64_t Lq, int Hq, int Hkv, int sets) {
-  return (Lq * (Hq / Hkv) + sets * kFewRows - 1) / (sets * kFewRows);
-}
-
-// Splits wanted of u tiles for keys up to L.  A step of a workgroup's waves takes about
-// 1.8 us of a nearly empty chip and the join 0.22 us a split, so of w steps
-// more than sqrt(8 w) splits cost more than they give (one stream of 32768: 32
-// splits 21 us, 64 25, 128 37).
-int64_t splits_of(int64_t u, int64_t L, int64_t blocks) {
-  const int64_t w = (L + kFewKeys * kFewWaves - 1) / (kFewKeys * kFewWaves);
-  int64_t s = (blocks + u - 1) / u;
-  s = s < w ? s : w;
-  while (s > 1 && s * s > 8 * w) --s;
-  if (s <= 1) return 1;
-  const int64_t steps = (w + s - 1) / s;
-  return (w + steps - 1) / steps;
-}
-
-// Sixteens of rows that a wave takes.  Two spare every second key's decoding, but
-// take twice the registers and make the steps longer: only where a SIMD has 20
-// steps of 64 keys of 128 elements, 40 of 64 (32 rows of a key head, 128 key heads of
-// 128, 16000 keys: 109 -> 87 us; 32 of them 39.1 and 39.7; 8 and 4000 keys 13.0 and
-// 16.3.  Heads of 64: 62 -> 57, 25.1 and 28.8, 11.6 and 13.2.  Four at a time, 64 rows:
-// 269 us where two take 212.)
-int sets_of(const AttnArgs& a, int64_t L) {
-  if (a.Lq * (a.Hq / a.Hkv) <= kFewRows) return 1;
-  const int64_t steps = a.B * a.Hkv * tiles_of(a.Lq, a.Hq, a.Hkv, 1) * ((L + kFewKeys - 1) / kFewKeys);
-  return steps * a.D >= (int64_t)1024 * 20 * 128 ? 2 : 1;
-}
-
 }  // namespace
 
-size_t attn_few_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
-  const int64_t s = splits_of(B * Hkv * tiles_of(Lq, Hq, Hkv, 1), L, kFewBlocks);   // (a source may take fewer)
-  return s > 1 ? s * AttnSplit::bytes(B * Lq * Hq, D) : 0;
+// (of bf16 heads of 128 the launch takes fewer)
+size_t attn_few_ws_bytes(bool tree, int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L) {
+  return few_sums_bytes(few_plan(tree, false, B, Lq, Hq, Hkv, D, L).splits, B * Lq * Hq, D);
 }
 
 template <class Source>
 hipError_t launch_attn_few(const AttnArgs& a, const Source& src, int64_t L, void* ws,
                            size_t ws_bytes, hipStream_t stream) {
   const int64_t rows = a.B * a.Lq * a.Hq;
-  const int sets = Source::kTree ? sets_of(a, L) : 1;
-  const int64_t tiles = tiles_of(a.Lq, a.Hq, a.Hkv, sets);
-  int64_t s = splits_of(a.B * a.Hkv * tiles, L, !Source::kF16 && a.D == 128 ? kFewBlocksWide : kFewBlocks);
+  const FewPlan plan = few_plan(Source::kTree, !Source::kF16 && a.D == 128, a.B, a.Lq, a.Hq, a.Hkv, a.D, L);
+  const int64_t tiles = plan.tiles;
+  int64_t s = plan.splits;
   const int64_t fit = (int64_t)(ws_bytes / AttnSplit::bytes(rows, a.D));
   if (s > fit) s = fit > 1 ? fit : 1;
   const AttnSplit sp = AttnSplit::in(ws, s, rows, a.D);
@@ -607,7 +566,7 @@ hipError_t launch_attn_few(const AttnArgs& a, const Source& src, int64_t L, void
   const auto of = [&](auto once) {
     constexpr bool kOnce = decltype(once)::value;
     if constexpr (Source::kTree)
-      if (sets > 1) {
+      if (plan.sets > 1) {
         a.D == 64 ? go(attn_few_kernel<Source, 64, kOnce, 2>) : go(attn_few_kernel<Source, 128, kOnce, 2>);
         return;
       }
