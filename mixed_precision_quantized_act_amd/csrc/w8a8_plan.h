@@ -9,7 +9,12 @@
 namespace qact {
 
 // Few rows, or few outputs (w8a8_split.hip): tiles of 16 MT rows and 16 NT columns,
-// W waves with rings of S lines of 128 elements per row.
+// W waves with rings of S lines of 128 elements per row.  Each is the fastest of all ways at
+// some of 138 drawn sizes (rows x columns x K, us; the best of the others): 16 x 16 at 42 (2610 x
+// 5 x 13392 1.45 times ahead), 32 x 32 at 12 (7176 x 24 x 8992 1.24), 64 x 16 at 17
+// (9113 x 1 x 2032 5.4 and 6.5; 61 x 2943 x 288 4.1 and 4.5), 64 x 32 at 12 (64 x 7680
+// x 1920 6.8 and 8.4), 64 x 64 at 11 (14022 x 47 x 12288 29 and 49; the rating takes 64 x 32
+// there, 52).
 #define QACT_W8_SPLITS(X) X(1, 1, 4, 4) X(2, 2, 4, 4) X(4, 1, 4, 3) X(4, 2, 4, 3) X(4, 4, 4, 2)
 struct SplitShape {
   int mt, nt, waves, slots;
@@ -27,14 +32,22 @@ constexpr int split_smem(const SplitShape& s) {
 
 // Many rows (qgemm_w8a8.hip): tiles of 128 x 128 (two fit a compute unit), 256 x
 // 128, 192 x 256 and 256 x 256.  us: a tile's start and end and a unit of 64 of K, of
-// a tile alone and with all compute units busy.
+// a tile alone and with all compute units busy.  (256 x 128 one by one: 10374 x 590 x
+// 3584 32.6, the best of the others 35.6; 12698 x 549 x 2320 32.1 and 33.6.)
+//
+// Over the same sizes what is chosen takes 1.02 times the best on the geometric mean.  The rating
+// knows neither the outputs' type nor GELU (8192 x 8192 x 4096 to float32: 337, by 192 x 256 309).
 enum W8Tile { kTile128, kTile256x128, kTile192x256, kTile256, kTiles };
 constexpr int kTileRows[kTiles] = {128, 256, 192, 256}, kTileCols[kTiles] = {128, 128, 256, 256};
 constexpr int kTileFit[kTiles] = {2, 1, 1, 1};
-constexpr double kStartAlone[kTiles] = {2.5, 4.5, 5.5, 6.5}, kStartBusy[kTiles] = {3.2, 5.8, 6.2, 10.9};
-constexpr double kUnitAlone[kTiles] = {0.21, 0.36, 0.42, 0.50}, kUnitBusy[kTiles] = {0.28, 0.48, 0.65, 0.68};
-// 256 x 256 in a stream of whole rounds: start and end of the stream, end of a tile
-constexpr double kStreamStart = 4.0, kStreamEnd = 3.5, kStreamUnit = 0.80;
+constexpr double kStartAlone[kTiles] = {2.5, 4.5, 5.5, 6.5}, kStartBusy[kTiles] = {3.2, 5.8, 6.2, 6.5};
+constexpr double kUnitAlone[kTiles] = {0.21, 0.36, 0.42, 0.50}, kUnitBusy[kTiles] = {0.28, 0.48, 0.65, 0.80};
+// 256 x 256 in a stream of whole rounds: start and end of the stream, end of a tile.  A unit
+// costs a fiftieth more than one by one, so long K goes one by one, whose ends are
+// exposed (8192 x 8192, 4 rounds, one by one and in a stream: K 16384 869 and 885, 8192
+// 450 and 456, 4096 246 and 245, 2048 140 and 138; one round, 4096 x 4096 x 8192: 116 and
+// 118).  All at the power limit, where rated times are up to a tenth too short.
+constexpr double kStreamStart = 4.0, kStreamEnd = 3.0, kStreamUnit = 0.82;
 constexpr int kStreamLeast = 6;                  // units
 
 constexpr int64_t kW8Places = 256;               // compute units
