@@ -449,7 +449,9 @@ def rope_freqs(R, base=10000.0, stretch=STRETCH_NONE, factor=1.0, original=0, fa
     position, stretched to `factor` times the context; STRETCH_RAMP: of `original`
     positions."""
     import numpy as np
-    freq, scale = np.zeros(max(R, 0) // 2), ctypes.c_float()
+    # (ctypes keeps the lowest 32 bits of a larger R or stretch: the array would be another's)
+    R, stretch = min(max(R, 0), 65537), min(max(stretch, -1), STRETCH_RAMP + 1)
+    freq, scale = np.zeros(R // 2), ctypes.c_float()
     _check("qa_rope_freqs", lib().qa_rope_freqs(stretch, R, base, factor, original, fast, slow,
                                                 freq.ctypes.data, ctypes.addressof(scale)))
     return freq, scale.value
