@@ -482,7 +482,8 @@ int qk_norm_rope(const uint16_t* q, int64_t ldq, int Hq, const uint16_t* k, int6
  *   QA_STRETCH_NONE    f_i = base^(-2 i / R)
  *   QA_STRETCH_LINEAR  f_i / factor (positions interpolated)
  *   QA_STRETCH_BASE    the base times factor^(R / (R - 2)): the slowest pair is
- *                      stretched by factor, the fastest not at all (R > 2)
+ *                      stretched by factor, the fastest not at all (R > 2; a base
+ *                      beyond float64 is refused)
  *   QA_STRETCH_RAMP    (Peng et al., arXiv 2309.00071) a pair that turns more than
  *                      `fast` times over the `original` positions keeps f_i, one
  *                      that turns fewer than `slow` times takes f_i / factor, and

@@ -840,8 +840,9 @@ int qa_rope_freqs(qa_stretch kind, int R, double base, double factor, double ori
   const bool ramp = kind == QA_STRETCH_RAMP;
   if (ramp && !(original > 0.0 && std::isfinite(original) && slow > 0.0 && fast >= slow && std::isfinite(fast)))
     return QA_EINVAL;
-  if (scale) *scale = ramp && factor > 1.0 ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
   const double b = kind == QA_STRETCH_BASE ? base * std::pow(factor, (double)R / (R - 2)) : base;
+  if (!std::isfinite(b)) return QA_EINVAL;
+  if (scale) *scale = ramp && factor > 1.0 ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
   double low = 0.0, high = 0.0;
   if (ramp) {
     const auto at = [&](double turns) {

@@ -21,3 +21,13 @@ def test_kinds(stretch):
 
 def test_the_largest_and_the_smallest():
     assert qa.rope_freqs(65536)[0].shape == (32768,) and qa.rope_freqs(2)[0].shape == (1,)
+
+
+@pytest.mark.parametrize("R,factor", [(4, 1e155), (64, 1e300), (6, 1e204)])
+def test_a_stretched_base_beyond_float64(R, factor):
+    """(Its frequencies would be zeros but for the first.)"""
+    with pytest.raises(qa.QactError) as e:
+        qa.rope_freqs(R, 10000.0, qa.STRETCH_BASE, factor=factor)
+    assert e.value.status == EINVAL
+    f, _ = qa.rope_freqs(R, 10000.0, qa.STRETCH_BASE, factor=1e100)
+    assert (f > 0).all()
