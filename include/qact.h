@@ -421,11 +421,13 @@ int qlinear_bf16(const uint16_t* x, int64_t ldx, const uint8_t* w_q, const uint8
  * a_q i8 [M][K], a_s f32 [M] and w_q i8 [N][K], w_s f32 [N], as act_quant INT8
  * makes both (any codes, -128 too; a_q, w_q 16-byte aligned); bias, y, out and
  * epi as for qlinear_nvfp4.  The sum is an exact int32; it is rounded once to
- * float32, then multiplied by w_s[n] and by a_s[m] (one rounding each), + bias.
+ * float32 and once more times w_s[n]; the product with a_s[m] and the bias are one
+ * fused operation with one rounding.
  * K a multiple of 16 below 2^17 (QA_ESHAPE otherwise), M and N as for
  * qlinear_nvfp4.  ws: with qlinear_w8a8_workspace() bytes (0 for many sizes) the
  * sums of few output tiles are split along K; less (also none) splits less, with
- * the same results bit for bit.
+ * the same results bit for bit.  Calls (and replayed graphs) that may run at the same
+ * time need workspaces of their own.
  * ------------------------------------------------------------------------ */
 size_t qlinear_w8a8_workspace(int64_t M, int64_t N, int64_t K);
 int qlinear_w8a8(const int8_t* a_q, const float* a_s, const int8_t* w_q, const float* w_s, int64_t M,
@@ -586,8 +588,8 @@ int attn_kv4(const uint16_t* q, int64_t ldq, int64_t B, int64_t Lq, int Hq, int 
  * and values of all heads, as if all were read before any is written (so path may
  * name a position twice, in any order).  Where either position has no slot
  * nothing is written; every other slot stays as it was.  path int32 [B][T].
- * 0 <= T <= 1024, B H < 2^24.  Streams that share a page that is written here
- * leave a mix of their tokens there. */
+ * 0 <= T <= 1024, B H < 2^24.  Where a page that is written here stands twice in the
+ * table, of one stream or of two, a mix of their tokens may be left there. */
 size_t attn_kv4_tree_workspace(int64_t B, int64_t Lq, int Hq, int H, int D, int64_t max_len);
 int attn_kv4_tree(const uint16_t* q, int64_t ldq, int64_t B, int64_t Lq, int Hq, int H, int D,
                   const uint8_t* k_q, const uint8_t* k_s, const uint8_t* v_q, const uint8_t* v_s,

@@ -329,7 +329,7 @@ template <class Source>
 hipError_t launch_attn_tile(const AttnArgs& a, const Source& src, int64_t L, void* ws,
                             size_t ws_bytes, hipStream_t stream);
 
-// A tree's rows, at most 128 a key head (attn_tree.hip).
+// A tree's rows, many of a key head (attn_tree.hip).
 size_t attn_tree_ws_bytes(int64_t B, int64_t Lq, int Hq, int Hkv, int D, int64_t L);
 hipError_t launch_attn_tree(const AttnArgs& a, const Kv4TreeSource& src, int64_t L, void* ws, size_t ws_bytes,
                             hipStream_t stream);

@@ -13,9 +13,9 @@
 // end.
 //
 // 16 streams of 32 tokens over 16384 to 32768 keys, 32 query and 8 key heads of 128 (128 rows):
-// 288 us, 201 GFLOP at 0.70 PFLOP/s, 7 of them for the join; equal pieces 317; with
+// 288 us, 201 GFLOP at 0.70 PFLOP/s, 7 of them for the join; equal pieces a tenth more; with
 // the waves of attn_tile.hip 353.  A tile of keys takes 1.28 us, a unit's start and end 10: MFMA busy
-// 0.34 of the cycles, VALU 0.40 (a third of it decoding), shared memory 0.32, a wave
+// 0.34 of the cycles, VALU 0.42 (a third of it decoding), shared memory 0.33, a wave
 // waiting 0.26 of its time, at 2.4 GHz.  3 streams of 250 tokens over up to 8191 keys, 30 heads of
 // 64 (256 rows): 72 to 76 us, a tile 1.1 to 1.4.
 #include "attn_rows.h"
@@ -138,7 +138,7 @@ attn_tree_kernel(AttnArgs a, Kv4TreeSource src, TreeSums sp, int tiles, Gate gat
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), group = wave % kGroups, part = wave / kGroups;
   const int G = a.Hq / a.Hkv;
   // (of the two waves of a SIMD one ahead of the other, so that they want its units at
-  // different times: 281 -> 278 us, 3 streams of 250 tokens to 32000 keys 239 -> 234)
+  // different times: 1 per cent, 3 streams of 250 tokens to 32000 keys 2)
   if (wave >= kTreeWaves / 2) __builtin_amdgcn_s_setprio(1);
 
   if (tid < kHalf / 16) *reinterpret_cast<u32x4*>(vt + 3 * kBytes + 16 * tid) = u32x4{0, 0, 0, 0};
@@ -607,8 +607,8 @@ double tree_join_time(int64_t sums, int rows, int D) { return 4.0 + (double)sums
 // How `units` of `len` tiles are cut: the time of n equal pieces is that of their
 // rounds, the shares' that of what each compute unit has.  Streams of one length
 // are assumed, and the shares taken up to a tenth more: they stay as good where the
-// lengths differ (16 streams of 16384 to 32768 keys, 8 key heads of 128, 128 rows: 317 us
-// in two pieces each, 279 in shares; all of 32000, 4 streams of 16 key heads: 180
+// lengths differ (16 streams of 16384 to 32768 keys, 8 key heads of 128, 128 rows: 1.1 times
+// as long in two pieces each as in shares; all of 32000, 4 streams of 16 key heads: 180
 // and 180; of 8000: 56 and 59; of 4000: 37 and 40).
 struct TreeCut {
   int shares, pieces;

@@ -11,9 +11,9 @@
 // half as large need half as much again and were 15 % slower (two of them on a
 // compute unit, to hide each other's ends: 17776 rows of 7680 against 1920 320 us).
 //
-// What bounds it is power: 17776 rows of 1920 against 5760 take 199 us (1.98 POP/s, a
-// library's product 254), of 7680 against 1920 246 us (2.13 POP/s; 256).  The clock
-// goes down to 1.63 GHz with the matrix units busy 0.63 of the cycles; with zeros as
+// What bounds it is power: 17776 rows of 1920 against 5760 take 200 us (1.97 POP/s, a
+// library's product 235 to 254), of 7680 against 1920 255 us (2.05 POP/s; 254 to 257), both
+// with a bias.  The clock goes down to 1.63 GHz with the matrix units busy 0.63 of the cycles; with zeros as
 // operands the same launches take 186 and 211 us.
 #include "w8a8.h"
 

@@ -14,10 +14,10 @@
 // tokens, forms each token's R/2 sines and cosines once, in shared memory, for
 // all its heads, and has the heads' elements on their way meanwhile: one thread two
 // vectors, so that many small workgroups hide each other's waits.  17776 tokens of 30 +
-// 30 heads of 64 (273 MB): 50 us, 5.4 TB/s, where a large copy reaches 5.1; workgroups of 64,
-// 256 and 512 threads 54, 52 and 52; four times the vectors a thread 57; stores past the
-// caches 73 (half the head turned) and 54 (all of it).  63 tokens of 32 + 8 heads of 128: 5 us,
-// a launch.
+// 30 heads of 64 (273 MB): 54.5 us, 5.0 TB/s, where a large copy reaches 5.1.  In a loop over
+// three sets of buffers it takes 50, workgroups of 64, 256 and 512 threads 54, 52 and 52, four
+// times the vectors a thread 57, stores past the caches 73 (half the head turned) and 54 (all
+// of it).  63 tokens of 32 + 8 heads of 128: 4.1 us, a launch.
 #include "qact_device.h"
 #include "qact_internal.h"
 
